@@ -104,6 +104,13 @@ def lib() -> ctypes.CDLL:
             "cas_f32_to_bf16": ([P, i64, P, P], i32),
             "cas_argmax": ([P, i32, i64, P, P], i32),
             "cas_embed": ([P, i32, P, i64, i32, P, P], i32),
+            "cas_qk_norm_rope": ([P, i32, i32, i32, i32, P, P, ctypes.c_float, P, i64, i32, ctypes.c_double, P, P, i64,
+                                  P, i64, P], i32),
+            "cas_paged_append": ([P, P, P, i32, i32, P, P, ctypes.c_float, ctypes.c_double, P, P], i32),
+            "cas_paged_attn": ([P, P, P, i32, P, P, u64, P], i32),
+            "cas_paged_attn_workspace_bytes": ([i32, i32, i32], u64),
+            "cas_spec_verify": ([P, i64, P, i64, P, P, P, i32, i32, i64, ctypes.c_double, P, P, P, P, u64, P], i32),
+            "cas_spec_verify_workspace_bytes": ([i32, i32, i64], u64),
             "cas_draft_attn_decode_noalloc": ([P, i32, P, i32, P, P, i32, P, P], i32),
         }
         for name, (args, res) in sig.items():
@@ -668,3 +675,213 @@ def embed(tokens: torch.Tensor, table: torch.Tensor, stream=None) -> torch.Tenso
     x = torch.empty(tokens.numel(), dim, dtype=torch.float32, device=table.device)
     _check(lib().cas_embed(_ptr(tokens), tokens.numel(), _ptr(table), V, dim, _ptr(x), _stream(stream)), "cas_embed")
     return x
+
+
+T_F32, T_BF16 = 0, 1  # element types of an input that may be either
+
+
+def _qkv(t: torch.Tensor, n_q_heads: int, n_kv_heads: int, what: str) -> int:
+    """Checks a fused QKV product and returns its element type."""
+    if t.dim() != 2 or t.shape[1] != (n_q_heads + 2 * n_kv_heads) * 128:
+        raise ValueError(f"{what}: qkv must be [rows][(n_q_heads + 2 n_kv_heads) * 128]")
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{what}: qkv must be fp32 or bfloat16")
+    return T_BF16 if t.dtype == torch.bfloat16 else T_F32
+
+
+def _on(dev: torch.device, *tensors):
+    """Raises unless every given tensor is on dev."""
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {t.device} and {dev}: one device expected")
+
+
+def _gamma(g: torch.Tensor | None, what: str) -> torch.Tensor | None:
+    if g is None:
+        return None
+    g = _bits(g)
+    _shape(g, (128,), what)
+    return g
+
+
+def _head_rows(t: torch.Tensor, rows: int, heads: int, what: str) -> tuple[ctypes.c_void_p, int]:
+    """Pointer and row stride of bf16 rows [rows][heads][128] that may lie in a larger buffer."""
+    t = _bits(t)
+    _shape(t, (rows, heads, 128), what)
+    if not t.is_cuda:
+        raise ValueError("libcas takes device tensors")
+    if rows and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != 128)):
+        raise ValueError(f"{what}: the heads of a row must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if rows > 1 else heads * 128
+
+
+def qk_norm_rope(qkv: torch.Tensor, n_q_heads: int, n_kv_heads: int, gamma_q: torch.Tensor | None = None,
+                 gamma_k: torch.Tensor | None = None, eps: float = 1e-6, pos: torch.Tensor | None = None,
+                 pos0: int = 0, rows_per_seq: int | None = None, theta: float = 1000000.0,
+                 q: torch.Tensor | None = None, k: torch.Tensor | None = None, v: torch.Tensor | None = None,
+                 stream=None):
+    """rope_split with an RMSNorm of every q and k head first (a gamma of None:
+    no norm). qkv: fp32 or bfloat16 [rows][(Hq+2Hkv)*128]; pos: int32 [rows], or
+    pos0 + row % rows_per_seq. Returns (q, k, v) bf16 bit patterns
+    [rows][H][128]; k and v may be given as rows of larger buffers."""
+    kind = _qkv(qkv, n_q_heads, n_kv_heads, "qk_norm_rope")
+    rows, dev = qkv.shape[0], qkv.device
+    gamma_q, gamma_k = _gamma(gamma_q, "gamma_q"), _gamma(gamma_k, "gamma_k")
+    if pos is not None and (pos.dtype != torch.int32 or tuple(pos.shape) != (rows,)):
+        raise ValueError("qk_norm_rope: pos must be int32 [rows]")
+    if q is None:
+        q = torch.empty(rows, n_q_heads, 128, dtype=torch.int16, device=dev)
+    if k is None:
+        k = torch.empty(rows, n_kv_heads, 128, dtype=torch.int16, device=dev)
+    if v is None:
+        v = torch.empty(rows, n_kv_heads, 128, dtype=torch.int16, device=dev)
+    _shape(_bits(q), (rows, n_q_heads, 128), "q")
+    _on(dev, gamma_q, gamma_k, pos, q, k, v)
+    kp, ks = _head_rows(k, rows, n_kv_heads, "k")
+    vp, vs = _head_rows(v, rows, n_kv_heads, "v")
+    with torch.cuda.device(dev):
+        _check(lib().cas_qk_norm_rope(_ptr(qkv), kind, rows, n_q_heads, n_kv_heads, _ptr(gamma_q), _ptr(gamma_k),
+                                      float(eps), _ptr(pos), pos0, rows_per_seq or max(rows, 1), float(theta),
+                                      _ptr(q), kp, ks, vp, vs, _stream(stream)), "cas_qk_norm_rope")
+    return q, k, v
+
+
+# ------------------------------------------------------------------ paged cache
+class cas_paged_kv(ctypes.Structure):
+    _fields_ = [("n_kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class cas_paged_batch(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("reserved0", ctypes.c_int32), ("row_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("pages", ctypes.c_void_p)]
+
+
+def _paged(rows: int, k_pages, v_pages, row_start, kv_len, pages, dev):
+    """Descriptors of a paged cache (pools [n_pages][page_size][H][128], any
+    strides with contiguous heads) and its ragged batch."""
+    k, v = _bits(k_pages), _bits(v_pages)
+    if k.dim() != 4 or k.shape[3] != 128 or v.shape != k.shape:
+        raise ValueError("k_pages and v_pages: [n_pages][page_size][n_kv_heads][128] of one shape")
+    if k.stride() != v.stride() or k.stride(3) != 1:
+        raise ValueError("k_pages and v_pages: equal strides with contiguous heads expected")
+    batch = kv_len.numel()
+    for t, shape, what in ((row_start, (batch + 1,), "row_start"), (kv_len, (batch,), "kv_len")):
+        if t.dtype != torch.int32:
+            raise ValueError(f"{what}: int32 expected")
+        _shape(t, shape, what)
+    if pages.dtype != torch.int32 or pages.dim() != 2 or pages.shape[0] != batch:
+        raise ValueError("pages: int32 [batch][max_pages] expected")
+    _on(dev, k, v, row_start, kv_len, pages)
+    if not k.is_cuda:
+        raise ValueError("libcas takes device tensors")
+    n, size, heads, _ = k.shape
+    # a stride over an extent of one is never used, and torch may report any
+    sp, st, sh = (k.stride(i) if k.shape[i] > 1 else 128 for i in range(3))
+    kv = cas_paged_kv(heads, size, n, k.data_ptr(), v.data_ptr(), sp, st, sh)
+    return kv, cas_paged_batch(batch, rows, pages.shape[1], 0, _ptr(row_start), _ptr(kv_len), _ptr(pages))
+
+
+def paged_append(qkv: torch.Tensor, n_q_heads: int, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                 row_start: torch.Tensor, kv_len: torch.Tensor, pages: torch.Tensor,
+                 gamma_q: torch.Tensor | None = None, gamma_k: torch.Tensor | None = None, eps: float = 1e-6,
+                 theta: float = 1000000.0, q: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Splits, norms (gammas given) and rotates a fused QKV product of a ragged
+    batch and writes its keys and values into their cache slots; returns q
+    bf16 bit patterns [rows][n_q_heads][128]. kv_len counts the rows' tokens."""
+    kind = _qkv(qkv, n_q_heads, k_pages.shape[2], "paged_append")
+    rows, dev = qkv.shape[0], qkv.device
+    gamma_q, gamma_k = _gamma(gamma_q, "gamma_q"), _gamma(gamma_k, "gamma_k")
+    if q is None:
+        q = torch.empty(rows, n_q_heads, 128, dtype=torch.int16, device=dev)
+    _shape(_bits(q), (rows, n_q_heads, 128), "q")
+    _on(dev, gamma_q, gamma_k, q)
+    kv, b = _paged(rows, k_pages, v_pages, row_start, kv_len, pages, dev)
+    with torch.cuda.device(dev):
+        _check(lib().cas_paged_append(ctypes.byref(kv), ctypes.byref(b), _ptr(qkv), kind, n_q_heads, _ptr(gamma_q),
+                                      _ptr(gamma_k), float(eps), float(theta), _ptr(q), _stream(stream)),
+               "cas_paged_append")
+    return q
+
+
+def cas_paged_attn_workspace_bytes(rows: int, n_q_heads: int, n_kv_heads: int) -> int:
+    return int(lib().cas_paged_attn_workspace_bytes(rows, n_q_heads, n_kv_heads))
+
+
+def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, row_start: torch.Tensor,
+               kv_len: torch.Tensor, pages: torch.Tensor, out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """q [rows][Hq][128] -> o bf16 bit patterns [rows][Hq][128] over the paged
+    cache: every row sees its sequence's positions up to its own."""
+    q = _bits(q).contiguous()
+    _shape(q, (q.shape[0], q.shape[1], 128), "q")
+    rows, Hq, _ = q.shape
+    dev = q.device
+    if out is None:
+        out = torch.empty(rows, Hq, 128, dtype=torch.int16, device=dev)
+    _out(out, rows * Hq * 128, (torch.int16, torch.uint16, torch.bfloat16), "out")
+    kv, b = _paged(rows, k_pages, v_pages, row_start, kv_len, pages, dev)
+    if workspace is None:
+        workspace = torch.empty(cas_paged_attn_workspace_bytes(rows, Hq, kv.n_kv_heads), dtype=torch.uint8, device=dev)
+    _on(dev, out, workspace)
+    with torch.cuda.device(dev):
+        _check(lib().cas_paged_attn(ctypes.byref(kv), ctypes.byref(b), _ptr(q), Hq, _ptr(out), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(stream)), "cas_paged_attn")
+    return out
+
+
+# ------------------------------------------------------------------ acceptance of drafted tokens
+def cas_spec_verify_workspace_bytes(batch: int, gamma: int, vocab: int) -> int:
+    return int(lib().cas_spec_verify_workspace_bytes(batch, gamma, vocab))
+
+
+def _logit_rows(t: torch.Tensor, batch: int, rows: int, vocab: int, what: str) -> tuple[ctypes.c_void_p, int]:
+    """Pointer and row stride of fp32 logits [batch][rows][vocab] in evenly spaced rows."""
+    if t.dtype != torch.float32:
+        raise ValueError(f"{what}: fp32 logits expected")
+    _shape(t, (batch, rows, vocab), what)
+    if not t.is_cuda:
+        raise ValueError("libcas takes device tensors")
+    step = t.stride(1) if rows > 1 else t.stride(0) if batch > 1 else vocab
+    if t.numel() and ((vocab > 1 and t.stride(2) != 1) or (rows > 1 and batch > 1 and t.stride(0) != rows * step)):
+        raise ValueError(f"{what}: evenly spaced contiguous rows expected")
+    return ctypes.c_void_p(t.data_ptr()), max(step, vocab)
+
+
+def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, x: torch.Tensor, u: torch.Tensor | None,
+                n_draft: torch.Tensor | None = None, temperature: float = 1.0, workspace: torch.Tensor | None = None,
+                stream=None):
+    """Judges drafted tokens x int32 [B][gamma] (the first n_draft[b] of them)
+    by target logits [B][gamma + 1][V], draft logits [B][gamma][V] and uniform
+    numbers u [B][gamma + 1]. Returns (n_accepted int32 [B], tokens int32
+    [B][gamma + 1]: the accepted, the next and -1 behind, ratio fp32
+    [B][gamma]). temperature 0 is greedy; draft and u may then be None."""
+    if x.dtype != torch.int32 or x.dim() != 2:
+        raise ValueError("spec_verify: x must be int32 [batch][gamma]")
+    B, G = x.shape
+    V, dev = target.shape[-1], x.device
+    if temperature != 0 and (u is None or (draft is None and G > 0)):
+        raise ValueError("spec_verify: draft and u are needed unless temperature is 0")
+    if u is not None and u.dtype != torch.float32:
+        raise ValueError("spec_verify: u must be fp32")
+    if u is not None:
+        _shape(u, (B, G + 1), "u")
+    if n_draft is not None:
+        if n_draft.dtype != torch.int32:
+            raise ValueError("spec_verify: n_draft must be int32")
+        _shape(n_draft, (B,), "n_draft")
+    _on(dev, target, draft, u, n_draft, workspace)
+    tp, ts = _logit_rows(target, B, G + 1, V, "target")
+    dp, ds = _logit_rows(draft, B, G, V, "draft") if draft is not None and G > 0 else (None, V)
+    n = torch.empty(B, dtype=torch.int32, device=dev)
+    tokens = torch.empty(B, G + 1, dtype=torch.int32, device=dev)
+    ratio = torch.empty(B, G, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(cas_spec_verify_workspace_bytes(B, G, V), dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().cas_spec_verify(tp, ts, dp, ds, _ptr(x), _ptr(u), _ptr(n_draft), B, G, V, float(temperature),
+                                     _ptr(n), _ptr(tokens), _ptr(ratio), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), _stream(stream)), "cas_spec_verify")
+    return n, tokens, ratio

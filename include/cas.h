@@ -444,6 +444,137 @@ int cas_argmax(const float* logits, int rows, int64_t vocab, int32_t* out, void*
 int cas_embed(const int32_t* tokens, int rows, const uint16_t* table, int64_t vocab, int dim, float* x,
               void* stream);
 
+/* Element types of inputs that may be the fp32 output of this library's
+ * products or the bf16 output of another one. */
+enum {
+  CAS_T_F32 = 0,
+  CAS_T_BF16 = 1
+};
+
+/* Split of a fused QKV product with an RMSNorm of every q and k head and the
+ * rotary embedding in the same pass (Qwen3-8B normalises its q and k heads;
+ * head_dim 128). qkv: [rows][(n_q_heads + 2 n_kv_heads) * 128] of qkv_type
+ * (CAS_T_F32 or CAS_T_BF16), q heads then k heads then v heads. A q head x
+ * becomes rot(x / sqrt(mean(x^2) + eps) * gamma_q), a k head the same with
+ * gamma_k; gamma_q, gamma_k: bf16 [128], NULL for no norm. rot turns the pair
+ * (i, i + 64) as in cas_rope_split by the angle p * theta^(-i/64), reduced
+ * exactly modulo a turn in 64-bit fixed point; row r has position p = pos[r]
+ * (int32 [rows], any value), or pos0 + r % rows_per_seq when pos is NULL. fp32
+ * arithmetic; outputs bf16, rounded once: q [rows][n_q_heads][128]; k and v
+ * rows of n_kv_heads * 128 values at strides k_row_stride / v_row_stride
+ * elements (multiples of 8, at least n_kv_heads * 128). A row never depends
+ * on another. Errors: CAS_ERR_INVALID for rows < 0, head counts < 1 or above
+ * 4096, an unknown type, theta not above 1, a negative or NaN eps, pos0 < 0 or
+ * rows_per_seq < 1 without pos, a null or misaligned pointer or a bad stride;
+ * CAS_ERR_CUDA. rows = 0 does nothing. */
+int cas_qk_norm_rope(const void* qkv, int qkv_type, int rows, int n_q_heads, int n_kv_heads, const uint16_t* gamma_q,
+                     const uint16_t* gamma_k, float eps, const int32_t* pos, int64_t pos0, int rows_per_seq,
+                     double theta, uint16_t* q, uint16_t* k, int64_t k_row_stride, uint16_t* v, int64_t v_row_stride,
+                     void* stream);
+
+/* Acceptance of drafted tokens (the end of a self-speculative step when
+ * tokens are sampled; [ABS] verified at full precision). For each of `batch`
+ * sequences gamma drafted tokens x, of which the first n_draft[b] count (NULL:
+ * all; clamped to 0..gamma), are judged by the target's and the draft's
+ * distributions
+ *   p_j(w) = exp((t_j(w) - max t_j) / temperature) / sum   (t: target logits)
+ *   q_j(w) = the same of the draft logits
+ * and given uniform numbers u in [0, 1):
+ *   ratio_j = min(1, p_j(x_j) / q_j(x_j)); x_j is accepted when all before it
+ *   were and u[b][j] < ratio_j; n = number accepted;
+ *   the next token is the lowest w with sum_{i <= w} r(i) > u[b][gamma] * R,
+ *   R = sum r, where r = p_n when n = n_draft[b], else max(p_n - q_n, 0), and
+ *   p_n again where that is zero everywhere.
+ * So the tokens follow the target's distribution. temperature 0 is greedy
+ * decoding: p_j is one at the lowest index of the largest logit, a drafted
+ * token is accepted when it is that index, and neither draft nor u is read
+ * (both may be NULL). target: fp32 rows (b, j), j <= gamma, at target +
+ * (b * (gamma + 1) + j) * target_stride; draft: rows (b, j), j < gamma, at
+ * draft + (b * gamma + j) * draft_stride; strides in elements, at least
+ * vocab. x: int32 [batch][gamma]; u: fp32 [batch][gamma + 1].
+ * n_accepted: int32 [batch]; tokens: int32 [batch][gamma + 1], the accepted
+ * tokens, the next token and -1 behind it; ratio: fp32 [batch][gamma] (NULL:
+ * not wanted), 0 behind n_draft[b].
+ * A NaN logit counts as -inf; infinite maxima share their row's mass. A row
+ * of nothing but -inf has p = 0: as the draft's it makes ratio 1 wherever the
+ * target has mass; as the target's nothing is accepted there and the next
+ * token is -1. A drafted token outside 0..vocab-1 has ratio 0, a NaN u accepts
+ * nothing, and u[b][gamma] outside [0, 1) takes the first or last token with
+ * r > 0. Sums are exact to about 2^-40: results depend on neither the order
+ * of additions nor the batch. Errors: CAS_ERR_INVALID for batch < 0 or above
+ * 65535, gamma outside 0..64, vocab outside 1..2^31-1, a stride below vocab, a
+ * temperature that is negative, NaN, infinite or positive but outside
+ * [1e-6, 1e6], or a null pointer; CAS_ERR_BUFFER if the workspace is null,
+ * misaligned or smaller than cas_spec_verify_workspace_bytes; CAS_ERR_CUDA.
+ * batch = 0 does nothing. */
+int cas_spec_verify(const float* target, int64_t target_stride, const float* draft, int64_t draft_stride,
+                    const int32_t* x, const float* u, const int32_t* n_draft, int batch, int gamma, int64_t vocab,
+                    double temperature, int32_t* n_accepted, int32_t* tokens, float* ratio, void* workspace,
+                    uint64_t workspace_bytes, void* stream);
+uint64_t cas_spec_verify_workspace_bytes(int batch, int gamma, int64_t vocab);
+
+/* ------------------------------------------------------------------ paged cache
+ * An uncompressed bf16 cache of one layer shared by many sequences: prompts
+ * are read in chunks of any length through it, before or without the encoding
+ * of cas_kv (whose verify attention takes at most 16 new tokens). The pools k
+ * and v hold n_pages pages of page_size tokens (a power of two, 8..1024) and
+ * n_kv_heads heads of 128 values: element (page, slot, head, d) is at
+ * page * page_stride + slot * token_stride + head * head_stride + d, strides
+ * in elements, multiples of 8 and at least 128, so pages may hold heads before
+ * tokens or K and V next to each other. Plain old data, owned by the caller. */
+typedef struct cas_paged_kv {
+  int32_t n_kv_heads, page_size;
+  int64_t n_pages;
+  uint16_t* k;
+  uint16_t* v;
+  int64_t page_stride, token_stride, head_stride;
+} cas_paged_kv;
+
+/* A ragged batch over a paged cache. Sequence b has the rows
+ * row_start[b] <= r < row_start[b + 1] (int32 [batch + 1], non-decreasing,
+ * values in 0..rows): its newest tokens, which are the last of its kv_len[b]
+ * (int32 [batch]) tokens in the cache; row r holds the token at position
+ * kv_len[b] - (row_start[b + 1] - r). Position p lies in page
+ * pages[b * max_pages + p / page_size] (int32 [batch][max_pages]), slot
+ * p % page_size. The three arrays are device memory, read when the kernels
+ * run, so a captured graph follows their values. Rows that belong to no
+ * sequence are left as they were. Device data out of range reads and writes
+ * nothing outside the buffers: positions from max_pages * page_size on are
+ * not written and not seen, a negative position writes nothing and sees no
+ * key, and a page id outside 0..n_pages-1 is not written and reads as zeros. */
+typedef struct cas_paged_batch {
+  int32_t batch, rows, max_pages, reserved0;
+  const int32_t* row_start;
+  const int32_t* kv_len;
+  const int32_t* pages;
+} cas_paged_batch;
+
+/* Appends the rows' keys and values to the paged cache, with the norms and the
+ * rotation of cas_qk_norm_rope on the way: qkv, gammas, eps and theta as
+ * there; the position of a row is its token's. K and V heads go to the
+ * token's slots, q to [rows][n_q_heads][128]. Two rows must not share a slot.
+ * Errors: those of cas_qk_norm_rope; CAS_ERR_INVALID for a null descriptor
+ * or pointer, a page size, stride or alignment out of range, batch < 0 or
+ * max_pages < 1. rows = 0 or batch = 0 does nothing. */
+int cas_paged_append(const cas_paged_kv* kv, const cas_paged_batch* b, const void* qkv, int qkv_type, int n_q_heads,
+                     const uint16_t* gamma_q, const uint16_t* gamma_k, float eps, double theta, uint16_t* q,
+                     void* stream);
+
+/* Attention of each sequence's new tokens over its paged cache (which holds
+ * them already): o = softmax(q K^T / sqrt(128)) V over the positions up to
+ * and including the row's own. Rows of one token (decoding), a few (drafted
+ * tokens) and long chunks of a prompt may share a batch. GQA: head h reads kv
+ * head h / (n_q_heads / n_kv_heads). q, o: bf16 [rows][n_q_heads][128]; fp32
+ * scores, statistics and sums, probabilities rounded to bf16 for the tensor
+ * cores. A row that sees no key is zero. Errors: CAS_ERR_INVALID for the
+ * descriptors as in cas_paged_append, n_q_heads not a multiple of n_kv_heads
+ * or a null or misaligned q or o; CAS_ERR_BUFFER if the workspace is null, not
+ * 16-byte aligned or smaller than cas_paged_attn_workspace_bytes;
+ * CAS_ERR_CUDA. rows = 0 or batch = 0 does nothing. */
+int cas_paged_attn(const cas_paged_kv* kv, const cas_paged_batch* b, const uint16_t* q, int n_q_heads, uint16_t* o,
+                   void* workspace, uint64_t workspace_bytes, void* stream);
+uint64_t cas_paged_attn_workspace_bytes(int rows, int n_q_heads, int n_kv_heads);
+
 #ifdef __cplusplus
 }
 #endif
