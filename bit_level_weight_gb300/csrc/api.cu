@@ -32,6 +32,7 @@ extern "C" int32_t cas_keep_from_ratio(double r) {
 
 namespace cas {
 int gemv_wait_status(bool clear);
+int attn_wait_status(bool clear);
 int set_first_wait_spins(uint32_t spins);
 void set_launch_overlap(bool on);
 }  // namespace cas
@@ -49,6 +50,8 @@ extern "C" int cas_set_launch_overlap(int on) {
 extern "C" int cas_device_status(void* stream) {
   if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return CAS_ERR_CUDA;
   int s = cas::gemv_wait_status(true);
+  const int w = cas::attn_wait_status(true);
+  if (!s) s = w;
   const int c[3] = {cas::corrupt_status_gemv(true), cas::corrupt_status_gemm(true), cas::corrupt_status_decode(true)};
   for (int v : c)
     if (!s) s = v;
