@@ -678,41 +678,72 @@ def embed(tokens: torch.Tensor, table: torch.Tensor, stream=None) -> torch.Tenso
 
 
 T_F32, T_BF16 = 0, 1  # element types of an input that may be either
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def _raw(t: torch.Tensor | None, index: int) -> int | None:
+    """Address of a contiguous tensor on device `index` (None: NULL)."""
+    if t is None:
+        return None
+    if t.get_device() != index:
+        raise ValueError(f"libcas takes device tensors of one device: got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError("libcas takes contiguous tensors")
+    return t.data_ptr()
+
+
+def _call(fn, what: str, index: int, stream, *args):
+    """Calls a C entry point on device `index` and its current (or the given) stream."""
+    if index < 0:
+        raise ValueError("libcas takes device tensors")
+    st = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, st)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, st)
+    if status != CAS_OK:
+        raise CasError(status, what)
+
+
+def _is_bf16(t: torch.Tensor, shape: tuple, what: str):
+    """Raises unless t holds bf16 values or bit patterns of exactly `shape`."""
+    if t.dtype not in _BF16:
+        raise ValueError(f"{what}: bf16 data must be bfloat16 or int16 bit patterns")
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
+
+
+def _is_i32(t: torch.Tensor, shape: tuple, what: str):
+    if t.dtype != torch.int32 or t.shape != shape:
+        raise ValueError(f"{what}: int32 {shape} expected, got {t.dtype} {tuple(t.shape)}")
 
 
 def _qkv(t: torch.Tensor, n_q_heads: int, n_kv_heads: int, what: str) -> int:
     """Checks a fused QKV product and returns its element type."""
     if t.dim() != 2 or t.shape[1] != (n_q_heads + 2 * n_kv_heads) * 128:
         raise ValueError(f"{what}: qkv must be [rows][(n_q_heads + 2 n_kv_heads) * 128]")
-    if t.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"{what}: qkv must be fp32 or bfloat16")
-    return T_BF16 if t.dtype == torch.bfloat16 else T_F32
+    if t.dtype == torch.float32:
+        return T_F32
+    if t.dtype == torch.bfloat16:
+        return T_BF16
+    raise ValueError(f"{what}: qkv must be fp32 or bfloat16")
 
 
-def _on(dev: torch.device, *tensors):
-    """Raises unless every given tensor is on dev."""
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {t.device} and {dev}: one device expected")
+def _gammas(gamma_q, gamma_k):
+    for g, what in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
+        if g is not None:
+            _is_bf16(g, (128,), what)
 
 
-def _gamma(g: torch.Tensor | None, what: str) -> torch.Tensor | None:
-    if g is None:
-        return None
-    g = _bits(g)
-    _shape(g, (128,), what)
-    return g
-
-
-def _head_rows(t: torch.Tensor, rows: int, heads: int, what: str) -> tuple[ctypes.c_void_p, int]:
-    """Pointer and row stride of bf16 rows [rows][heads][128] that may lie in a larger buffer."""
-    t = _bits(t)
-    _shape(t, (rows, heads, 128), what)
-    if not t.is_cuda:
-        raise ValueError("libcas takes device tensors")
+def _head_rows(t: torch.Tensor, heads: int, index: int, what: str) -> tuple[int, int]:
+    """Address and row stride of bf16 rows [rows][heads][128] that may lie in a larger buffer."""
+    if t.get_device() != index:
+        raise ValueError(f"libcas takes device tensors of one device: got {t.device}")
+    rows = t.shape[0]
     if rows and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != 128)):
         raise ValueError(f"{what}: the heads of a row must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if rows > 1 else heads * 128
+    return t.data_ptr(), t.stride(0) if rows > 1 else heads * 128
 
 
 def qk_norm_rope(qkv: torch.Tensor, n_q_heads: int, n_kv_heads: int, gamma_q: torch.Tensor | None = None,
@@ -726,23 +757,27 @@ def qk_norm_rope(qkv: torch.Tensor, n_q_heads: int, n_kv_heads: int, gamma_q: to
     [rows][H][128]; k and v may be given as rows of larger buffers."""
     kind = _qkv(qkv, n_q_heads, n_kv_heads, "qk_norm_rope")
     rows, dev = qkv.shape[0], qkv.device
-    gamma_q, gamma_k = _gamma(gamma_q, "gamma_q"), _gamma(gamma_k, "gamma_k")
-    if pos is not None and (pos.dtype != torch.int32 or tuple(pos.shape) != (rows,)):
-        raise ValueError("qk_norm_rope: pos must be int32 [rows]")
+    _gammas(gamma_q, gamma_k)
+    if pos is not None:
+        _is_i32(pos, (rows,), "pos")
     if q is None:
-        q = torch.empty(rows, n_q_heads, 128, dtype=torch.int16, device=dev)
+        q = torch.empty((rows, n_q_heads, 128), dtype=torch.int16, device=dev)
+    else:
+        _is_bf16(q, (rows, n_q_heads, 128), "q")
     if k is None:
-        k = torch.empty(rows, n_kv_heads, 128, dtype=torch.int16, device=dev)
+        k = torch.empty((rows, n_kv_heads, 128), dtype=torch.int16, device=dev)
+    else:
+        _is_bf16(k, (rows, n_kv_heads, 128), "k")
     if v is None:
-        v = torch.empty(rows, n_kv_heads, 128, dtype=torch.int16, device=dev)
-    _shape(_bits(q), (rows, n_q_heads, 128), "q")
-    _on(dev, gamma_q, gamma_k, pos, q, k, v)
-    kp, ks = _head_rows(k, rows, n_kv_heads, "k")
-    vp, vs = _head_rows(v, rows, n_kv_heads, "v")
-    with torch.cuda.device(dev):
-        _check(lib().cas_qk_norm_rope(_ptr(qkv), kind, rows, n_q_heads, n_kv_heads, _ptr(gamma_q), _ptr(gamma_k),
-                                      float(eps), _ptr(pos), pos0, rows_per_seq or max(rows, 1), float(theta),
-                                      _ptr(q), kp, ks, vp, vs, _stream(stream)), "cas_qk_norm_rope")
+        v = torch.empty((rows, n_kv_heads, 128), dtype=torch.int16, device=dev)
+    else:
+        _is_bf16(v, (rows, n_kv_heads, 128), "v")
+    i = qkv.get_device()
+    kp, ks = _head_rows(k, n_kv_heads, i, "k")
+    vp, vs = _head_rows(v, n_kv_heads, i, "v")
+    _call(lib().cas_qk_norm_rope, "cas_qk_norm_rope", i, stream, _raw(qkv, i), kind, rows, n_q_heads, n_kv_heads,
+          _raw(gamma_q, i), _raw(gamma_k, i), eps, _raw(pos, i), pos0, rows_per_seq or max(rows, 1), theta,
+          _raw(q, i), kp, ks, vp, vs)
     return q, k, v
 
 
@@ -759,29 +794,26 @@ class cas_paged_batch(ctypes.Structure):
                 ("pages", ctypes.c_void_p)]
 
 
-def _paged(rows: int, k_pages, v_pages, row_start, kv_len, pages, dev):
+def _paged(rows: int, k: torch.Tensor, v: torch.Tensor, row_start, kv_len, pages, i: int):
     """Descriptors of a paged cache (pools [n_pages][page_size][H][128], any
     strides with contiguous heads) and its ragged batch."""
-    k, v = _bits(k_pages), _bits(v_pages)
-    if k.dim() != 4 or k.shape[3] != 128 or v.shape != k.shape:
-        raise ValueError("k_pages and v_pages: [n_pages][page_size][n_kv_heads][128] of one shape")
-    if k.stride() != v.stride() or k.stride(3) != 1:
+    if k.dtype not in _BF16 or v.dtype not in _BF16 or k.dim() != 4 or k.shape[3] != 128 or v.shape != k.shape:
+        raise ValueError("k_pages and v_pages: bf16 [n_pages][page_size][n_kv_heads][128] of one shape")
+    n, size, heads, _ = k.shape
+    sp, st, sh, sd = k.stride()
+    if v.stride() != (sp, st, sh, sd) or sd != 1:
         raise ValueError("k_pages and v_pages: equal strides with contiguous heads expected")
-    batch = kv_len.numel()
-    for t, shape, what in ((row_start, (batch + 1,), "row_start"), (kv_len, (batch,), "kv_len")):
-        if t.dtype != torch.int32:
-            raise ValueError(f"{what}: int32 expected")
-        _shape(t, shape, what)
+    batch = kv_len.shape[0] if kv_len.dim() == 1 else -1
+    _is_i32(row_start, (batch + 1,), "row_start")
+    _is_i32(kv_len, (batch,), "kv_len")
     if pages.dtype != torch.int32 or pages.dim() != 2 or pages.shape[0] != batch:
         raise ValueError("pages: int32 [batch][max_pages] expected")
-    _on(dev, k, v, row_start, kv_len, pages)
-    if not k.is_cuda:
-        raise ValueError("libcas takes device tensors")
-    n, size, heads, _ = k.shape
+    if k.get_device() != i or v.get_device() != i:
+        raise ValueError(f"libcas takes device tensors of one device: got {k.device} and {v.device}")
     # a stride over an extent of one is never used, and torch may report any
-    sp, st, sh = (k.stride(i) if k.shape[i] > 1 else 128 for i in range(3))
-    kv = cas_paged_kv(heads, size, n, k.data_ptr(), v.data_ptr(), sp, st, sh)
-    return kv, cas_paged_batch(batch, rows, pages.shape[1], 0, _ptr(row_start), _ptr(kv_len), _ptr(pages))
+    kv = cas_paged_kv(heads, size, n, k.data_ptr(), v.data_ptr(), sp if n > 1 else 128, st if size > 1 else 128,
+                      sh if heads > 1 else 128)
+    return kv, cas_paged_batch(batch, rows, pages.shape[1], 0, _raw(row_start, i), _raw(kv_len, i), _raw(pages, i))
 
 
 def paged_append(qkv: torch.Tensor, n_q_heads: int, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -790,24 +822,25 @@ def paged_append(qkv: torch.Tensor, n_q_heads: int, k_pages: torch.Tensor, v_pag
                  theta: float = 1000000.0, q: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Splits, norms (gammas given) and rotates a fused QKV product of a ragged
     batch and writes its keys and values into their cache slots; returns q
-    bf16 bit patterns [rows][n_q_heads][128]. kv_len counts the rows' tokens."""
+    bf16 bit patterns [rows][n_q_heads][128]. Sequence b has the rows
+    row_start[b] to row_start[b + 1] - 1, the last of its kv_len[b] tokens."""
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages: [n_pages][page_size][n_kv_heads][128] expected")
     kind = _qkv(qkv, n_q_heads, k_pages.shape[2], "paged_append")
-    rows, dev = qkv.shape[0], qkv.device
-    gamma_q, gamma_k = _gamma(gamma_q, "gamma_q"), _gamma(gamma_k, "gamma_k")
+    rows, i = qkv.shape[0], qkv.get_device()
+    _gammas(gamma_q, gamma_k)
     if q is None:
-        q = torch.empty(rows, n_q_heads, 128, dtype=torch.int16, device=dev)
-    _shape(_bits(q), (rows, n_q_heads, 128), "q")
-    _on(dev, gamma_q, gamma_k, q)
-    kv, b = _paged(rows, k_pages, v_pages, row_start, kv_len, pages, dev)
-    with torch.cuda.device(dev):
-        _check(lib().cas_paged_append(ctypes.byref(kv), ctypes.byref(b), _ptr(qkv), kind, n_q_heads, _ptr(gamma_q),
-                                      _ptr(gamma_k), float(eps), float(theta), _ptr(q), _stream(stream)),
-               "cas_paged_append")
+        q = torch.empty((rows, n_q_heads, 128), dtype=torch.int16, device=qkv.device)
+    else:
+        _is_bf16(q, (rows, n_q_heads, 128), "q")
+    kv, b = _paged(rows, k_pages, v_pages, row_start, kv_len, pages, i)
+    _call(lib().cas_paged_append, "cas_paged_append", i, stream, ctypes.byref(kv), ctypes.byref(b), _raw(qkv, i), kind,
+          n_q_heads, _raw(gamma_q, i), _raw(gamma_k, i), eps, theta, _raw(q, i))
     return q
 
 
 def cas_paged_attn_workspace_bytes(rows: int, n_q_heads: int, n_kv_heads: int) -> int:
-    return int(lib().cas_paged_attn_workspace_bytes(rows, n_q_heads, n_kv_heads))
+    return lib().cas_paged_attn_workspace_bytes(rows, n_q_heads, n_kv_heads)
 
 
 def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, row_start: torch.Tensor,
@@ -815,39 +848,42 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ro
                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """q [rows][Hq][128] -> o bf16 bit patterns [rows][Hq][128] over the paged
     cache: every row sees its sequence's positions up to its own."""
-    q = _bits(q).contiguous()
-    _shape(q, (q.shape[0], q.shape[1], 128), "q")
+    if q.dim() != 3:
+        raise ValueError("q: [rows][n_q_heads][128] expected")
     rows, Hq, _ = q.shape
-    dev = q.device
+    _is_bf16(q, (rows, Hq, 128), "q")
+    q = q.contiguous()
+    dev, i = q.device, q.get_device()
+    kv, b = _paged(rows, k_pages, v_pages, row_start, kv_len, pages, i)
     if out is None:
-        out = torch.empty(rows, Hq, 128, dtype=torch.int16, device=dev)
-    _out(out, rows * Hq * 128, (torch.int16, torch.uint16, torch.bfloat16), "out")
-    kv, b = _paged(rows, k_pages, v_pages, row_start, kv_len, pages, dev)
+        out = torch.empty((rows, Hq, 128), dtype=torch.int16, device=dev)
+    else:
+        _is_bf16(out, (rows, Hq, 128), "out")
+    L = lib()
     if workspace is None:
-        workspace = torch.empty(cas_paged_attn_workspace_bytes(rows, Hq, kv.n_kv_heads), dtype=torch.uint8, device=dev)
-    _on(dev, out, workspace)
-    with torch.cuda.device(dev):
-        _check(lib().cas_paged_attn(ctypes.byref(kv), ctypes.byref(b), _ptr(q), Hq, _ptr(out), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream)), "cas_paged_attn")
+        workspace = torch.empty(L.cas_paged_attn_workspace_bytes(rows, Hq, kv.n_kv_heads), dtype=torch.uint8,
+                                device=dev)
+    _call(L.cas_paged_attn, "cas_paged_attn", i, stream, ctypes.byref(kv), ctypes.byref(b), _raw(q, i), Hq,
+          _raw(out, i), _raw(workspace, i), workspace.numel() * workspace.element_size())
     return out
 
 
 # ------------------------------------------------------------------ acceptance of drafted tokens
 def cas_spec_verify_workspace_bytes(batch: int, gamma: int, vocab: int) -> int:
-    return int(lib().cas_spec_verify_workspace_bytes(batch, gamma, vocab))
+    return lib().cas_spec_verify_workspace_bytes(batch, gamma, vocab)
 
 
-def _logit_rows(t: torch.Tensor, batch: int, rows: int, vocab: int, what: str) -> tuple[ctypes.c_void_p, int]:
-    """Pointer and row stride of fp32 logits [batch][rows][vocab] in evenly spaced rows."""
-    if t.dtype != torch.float32:
-        raise ValueError(f"{what}: fp32 logits expected")
-    _shape(t, (batch, rows, vocab), what)
-    if not t.is_cuda:
-        raise ValueError("libcas takes device tensors")
-    step = t.stride(1) if rows > 1 else t.stride(0) if batch > 1 else vocab
-    if t.numel() and ((vocab > 1 and t.stride(2) != 1) or (rows > 1 and batch > 1 and t.stride(0) != rows * step)):
+def _logit_rows(t: torch.Tensor, batch: int, rows: int, vocab: int, i: int, what: str) -> tuple[int, int]:
+    """Address and row stride of fp32 logits [batch][rows][vocab] in evenly spaced rows."""
+    if t.dtype != torch.float32 or t.shape != (batch, rows, vocab):
+        raise ValueError(f"{what}: fp32 logits {(batch, rows, vocab)} expected, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != i:
+        raise ValueError(f"libcas takes device tensors of one device: got {t.device}")
+    sb, sr, sv = t.stride()
+    step = sr if rows > 1 else sb if batch > 1 else vocab
+    if batch and rows and ((vocab > 1 and sv != 1) or (rows > 1 and batch > 1 and sb != rows * step)):
         raise ValueError(f"{what}: evenly spaced contiguous rows expected")
-    return ctypes.c_void_p(t.data_ptr()), max(step, vocab)
+    return t.data_ptr(), max(step, vocab)
 
 
 def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, x: torch.Tensor, u: torch.Tensor | None,
@@ -861,27 +897,22 @@ def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, x: torch.Tenso
     if x.dtype != torch.int32 or x.dim() != 2:
         raise ValueError("spec_verify: x must be int32 [batch][gamma]")
     B, G = x.shape
-    V, dev = target.shape[-1], x.device
+    V, dev, i = target.shape[-1], x.device, x.get_device()
     if temperature != 0 and (u is None or (draft is None and G > 0)):
         raise ValueError("spec_verify: draft and u are needed unless temperature is 0")
-    if u is not None and u.dtype != torch.float32:
-        raise ValueError("spec_verify: u must be fp32")
-    if u is not None:
-        _shape(u, (B, G + 1), "u")
+    if u is not None and (u.dtype != torch.float32 or u.shape != (B, G + 1)):
+        raise ValueError("spec_verify: u must be fp32 [batch][gamma + 1]")
     if n_draft is not None:
-        if n_draft.dtype != torch.int32:
-            raise ValueError("spec_verify: n_draft must be int32")
-        _shape(n_draft, (B,), "n_draft")
-    _on(dev, target, draft, u, n_draft, workspace)
-    tp, ts = _logit_rows(target, B, G + 1, V, "target")
-    dp, ds = _logit_rows(draft, B, G, V, "draft") if draft is not None and G > 0 else (None, V)
+        _is_i32(n_draft, (B,), "n_draft")
+    tp, ts = _logit_rows(target, B, G + 1, V, i, "target")
+    dp, ds = _logit_rows(draft, B, G, V, i, "draft") if draft is not None and G > 0 else (None, V)
     n = torch.empty(B, dtype=torch.int32, device=dev)
-    tokens = torch.empty(B, G + 1, dtype=torch.int32, device=dev)
-    ratio = torch.empty(B, G, dtype=torch.float32, device=dev)
+    tokens = torch.empty((B, G + 1), dtype=torch.int32, device=dev)
+    ratio = torch.empty((B, G), dtype=torch.float32, device=dev)
+    L = lib()
     if workspace is None:
-        workspace = torch.empty(cas_spec_verify_workspace_bytes(B, G, V), dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib().cas_spec_verify(tp, ts, dp, ds, _ptr(x), _ptr(u), _ptr(n_draft), B, G, V, float(temperature),
-                                     _ptr(n), _ptr(tokens), _ptr(ratio), _ptr(workspace),
-                                     workspace.numel() * workspace.element_size(), _stream(stream)), "cas_spec_verify")
+        workspace = torch.empty(L.cas_spec_verify_workspace_bytes(B, G, V), dtype=torch.uint8, device=dev)
+    _call(L.cas_spec_verify, "cas_spec_verify", i, stream, tp, ts, dp, ds, _raw(x, i), _raw(u, i), _raw(n_draft, i), B,
+          G, V, temperature, n.data_ptr(), tokens.data_ptr(), ratio.data_ptr(), _raw(workspace, i),
+          workspace.numel() * workspace.element_size())
     return n, tokens, ratio

@@ -58,7 +58,10 @@ int check_paged(const cas_paged_kv* kv, const cas_paged_batch* b) {
 namespace {
 
 constexpr int kHeadsMax = 4096;
+constexpr int kHalfWarps = 64;  // wanted a SM before a half-warp takes more than one head
+constexpr int kHeadsPer = 12;   // heads a half-warp takes at most
 constexpr int kThreads = 256;
+constexpr int kAhead = 4;  // heads whose loads a half-warp has in flight
 
 struct QkArgs {
   const void* qkv;
@@ -73,15 +76,24 @@ struct QkArgs {
   uint64_t F[64];  // theta^(-i/64) / (2 pi) in units of 2^-64
 };
 
-__device__ __forceinline__ void load4(const float* p, float x[4]) {
-  const float4 t = *reinterpret_cast<const float4*>(p);
-  x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
-}
-__device__ __forceinline__ void load4(const uint16_t* p, float x[4]) {
-  const uint2 t = *reinterpret_cast<const uint2*>(p);
+__device__ __forceinline__ void unpack4(uint2 t, float x[4]) {
   x[0] = __uint_as_float(t.x << 16), x[1] = __uint_as_float(t.x & 0xFFFF0000u);
   x[2] = __uint_as_float(t.y << 16), x[3] = __uint_as_float(t.y & 0xFFFF0000u);
 }
+template <class T>
+struct Raw;  // four values as they were loaded
+template <>
+struct Raw<float> {
+  float4 t;
+  __device__ __forceinline__ void load(const float* p) { t = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void get(float x[4]) const { x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w; }
+};
+template <>
+struct Raw<uint16_t> {
+  uint2 t;
+  __device__ __forceinline__ void load(const uint16_t* p) { t = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void get(float x[4]) const { unpack4(t, x); }
+};
 __device__ __forceinline__ void store4(uint16_t* p, const float x[4]) {
   uint2 t;
   t.x = f2bf(x[0]) | (uint32_t)f2bf(x[1]) << 16;
@@ -104,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
   const int h0 = (int)(unit - row * per_row) * a.hpu, h1 = min(H, h0 + a.hpu);
   const int l = threadIdx.x & 15;
   const uint32_t half = (threadIdx.x & 16) ? 0xFFFF0000u : 0x0000FFFFu;
-  int64_t p, page = -1;
+  int64_t p, page = -1, slot = 0;
   int seq = 0;
   if (PAGED) {
     // the last sequence that starts at or before the row
@@ -118,6 +130,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
     if (row < s.start || row >= s.end) return;  // padding: left as it was
     p = (int64_t)s.len - (s.end - row);
     page = page_of(a.pg, seq, p);
+    slot = page * a.pg.page_stride + (p & ((1 << a.pg.shift) - 1)) * a.pg.token_stride;
   } else {
     p = a.pos ? (int64_t)a.pos[row] : a.pos0 + row % a.rps;
   }
@@ -129,52 +142,67 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
       sincospif((float)turn * 4.656612873077392578125e-10f /* 2^-31 */, &sn[j], &cs[j]);
     }
   }
+  const uint2 none = make_uint2(0, 0);
+  const uint2 gq0 = a.gq ? *reinterpret_cast<const uint2*>(a.gq + 4 * l) : none;
+  const uint2 gq1 = a.gq ? *reinterpret_cast<const uint2*>(a.gq + 64 + 4 * l) : none;
+  const uint2 gk0 = a.gk ? *reinterpret_cast<const uint2*>(a.gk + 4 * l) : none;
+  const uint2 gk1 = a.gk ? *reinterpret_cast<const uint2*>(a.gk + 64 + 4 * l) : none;
   const T* src = (const T*)a.qkv + row * H * CAS_BLK + 4 * l;
-  for (int h = h0; h < h1; ++h) {
-    float x[4], y[4];
-    load4(src + (int64_t)h * CAS_BLK, x);
-    load4(src + (int64_t)h * CAS_BLK + 64, y);
-    const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
-    const uint16_t* g = is_q ? a.gq : is_v ? nullptr : a.gk;
-    if (g) {
-      float ss = 0.f;
+  for (int hb = h0; hb < h1; hb += kAhead) {
+    Raw<T> rx[kAhead], ry[kAhead];  // loads of kAhead heads in flight
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ss = fmaf(x[j], x[j], fmaf(y[j], y[j], ss));
-#pragma unroll
-      for (int d = 8; d > 0; d >>= 1) ss += __shfl_xor_sync(half, ss, d);
-      const float inv = rsqrtf(ss * (1.f / CAS_BLK) + a.eps);
-      float gx[4], gy[4];
-      load4(g + 4 * l, gx);
-      load4(g + 64 + 4 * l, gy);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[j] *= inv * gx[j];
-        y[j] *= inv * gy[j];
+    for (int i = 0; i < kAhead; ++i)
+      if (hb + i < h1) {
+        rx[i].load(src + (int64_t)(hb + i) * CAS_BLK);
+        ry[i].load(src + (int64_t)(hb + i) * CAS_BLK + 64);
       }
-    }
-    if (!is_v) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float c = x[j], d = y[j];
-        x[j] = fmaf(c, cs[j], -d * sn[j]);
-        y[j] = fmaf(d, cs[j], c * sn[j]);
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = hb + i;
+      if (h >= h1) break;
+      float x[4], y[4];
+      rx[i].get(x);
+      ry[i].get(y);
+      const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
+      if (is_q ? a.gq != nullptr : !is_v && a.gk != nullptr) {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ss = fmaf(x[j], x[j], fmaf(y[j], y[j], ss));
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) ss += __shfl_xor_sync(half, ss, d);
+        const float inv = rsqrtf(ss * (1.f / CAS_BLK) + a.eps);
+        float gx[4], gy[4];
+        unpack4(is_q ? gq0 : gk0, gx);
+        unpack4(is_q ? gq1 : gk1, gy);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[j] *= inv * gx[j];
+          y[j] *= inv * gy[j];
+        }
       }
-    }
-    uint16_t* dst;
-    if (is_q) {
-      dst = a.q + (row * a.Hq + h) * CAS_BLK;
-    } else {
-      const int hk = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
-      if (PAGED) {
-        if (page < 0) continue;
-        dst = (is_v ? a.pg.v : a.pg.k) + page * a.pg.page_stride +
-              (p & ((1 << a.pg.shift) - 1)) * a.pg.token_stride + hk * a.pg.head_stride;
+      if (!is_v) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float c = x[j], d = y[j];
+          x[j] = fmaf(c, cs[j], -d * sn[j]);
+          y[j] = fmaf(d, cs[j], c * sn[j]);
+        }
+      }
+      uint16_t* dst;
+      if (is_q) {
+        dst = a.q + (row * a.Hq + h) * CAS_BLK;
       } else {
-        dst = is_v ? a.v + row * a.vs + (int64_t)hk * CAS_BLK : a.k + row * a.ks + (int64_t)hk * CAS_BLK;
+        const int hk = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
+        if (PAGED) {
+          if (page < 0) continue;
+          dst = (is_v ? a.pg.v : a.pg.k) + slot + hk * a.pg.head_stride;
+        } else {
+          dst = is_v ? a.v + row * a.vs + (int64_t)hk * CAS_BLK : a.k + row * a.ks + (int64_t)hk * CAS_BLK;
+        }
       }
+      store4(dst + 4 * l, x);
+      store4(dst + 64 + 4 * l, y);
     }
-    store4(dst + 4 * l, x);
-    store4(dst + 64 + 4 * l, y);
   }
 }
 
@@ -193,7 +221,10 @@ int launch_qk(QkArgs& a, int type, double theta, cudaStream_t st) {
   for (int i = 0; i < 64; ++i)  // below 2^64 / 6: the product is a whole number of 2^-64 turns
     a.F[i] = (uint64_t)std::llround(std::ldexp(std::exp(-lt * i / 64.0) / 6.283185307179586476925286766559, 62)) << 2;
   const int H = a.Hq + 2 * a.Hkv;
-  a.hpu = 1;
+  // A half-warp pays for its row's sines once, whatever number of heads it
+  // takes; few rows are spread over as many half-warps as there are heads.
+  const int64_t half_warps = (int64_t)sm_count() * kHalfWarps;
+  a.hpu = (int)std::min<int64_t>(kHeadsPer, std::max<int64_t>(1, (int64_t)a.rows * H / half_warps));
   const int64_t units = (int64_t)a.rows * ((H + a.hpu - 1) / a.hpu);
   const int64_t blocks = (units * 16 + kThreads - 1) / kThreads;
   if (blocks > 0x7FFFFFFF) return CAS_ERR_INVALID;
