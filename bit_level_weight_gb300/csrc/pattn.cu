@@ -23,10 +23,15 @@
 //                   thread), P back as bf16, O rescaled there when a row's
 //                   maximum grows by more than 2^8 (probabilities relative to
 //                   an older maximum are as exact), epilogue
-//   warp 8          TMA: K and V tiles from their pages, five 32 KB buffers
-//   warp 9          one thread issues tcgen05.mma: S = Q K^T (both from shared memory), O += P V
-//                   (P from tensor memory, V with the head dimension contiguous);
-//                   warps 10-11 complete its warpgroup and only give up registers
+//   warp 8, 10      TMA: K and V tiles from their pages, five 32 KB buffers
+//   warp 9          issues tcgen05.mma: S = Q K^T (both from shared memory),
+//                   O += P V (P from tensor memory, V with the head dimension
+//                   contiguous)
+//   warp 11         finds the CTA's units and hands them to the others one
+//                   ahead, with their Q rows
+//
+// Every wait is bounded: one that gives up marks the CTA, whose warps then
+// leave their loops, and sets a status that cas_device_status reads.
 //
 // Rounding: scores, statistics and sums are fp32; P is rounded to bf16 for the
 // product with V (2^-8 relative each, the size of the output's own rounding),
@@ -51,9 +56,9 @@ constexpr uint32_t kBuf = kTile * 256;     // bytes of a K or V tile
 constexpr uint32_t kHalf = kBuf / 2;       // 64 of the 128 dimensions
 constexpr int kThreads = 384;               // three warpgroups of 168 registers a thread at launch
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;  // 2 * 216 + 72 = 3 * 168: the softmax keeps a row of S
-constexpr int kMinTiles = 4;               // tiles a CTA takes at least
+constexpr int kMinCells = 3;               // cells of the line a CTA takes at least
 constexpr uint32_t kSpins = 1u << 20;
-constexpr int64_t kPieceFloats = kTile + 2;  // a row of a partial result: output, maximum, sum
+constexpr int64_t kPieceFloats = kTile + 2;  // floats a row of a partial result: output, maximum, sum
 
 __device__ int g_attn_status = 0;
 
@@ -61,9 +66,24 @@ struct AttnArgs {
   PagedDev d;
   const uint16_t* q;
   uint16_t* o;
-  float* ws;  // [2 * grid][piece_rows] rows of 128 + 2 floats
+  struct Cut* cuts;  // [grid]: the unit that the cut behind CTA c is the first one in
+  float* ws;         // [2 * grid] pieces of piece_rows rows: output [32][rows][4], maximum [rows], sum [rows]
   int Hq, G, piece_rows;
+  uint32_t gmul;     // f / G = (umulhi(f, gmul) + f) >> gshift for 0 <= f < 2^31
+  int gshift;
+  bool wide;         // o is 32-byte aligned
 };
+struct Cut {
+  int pieces;        // of the unit, CTAs c .. c + pieces - 1; 0: none
+  int start, hk, f0, rows, first;  // first row of the sequence, kv head, flat rows; the first piece's place
+};
+__device__ __forceinline__ int div_g(const AttnArgs& a, int f) {
+  return (int)((__umulhi((uint32_t)f, a.gmul) + (uint32_t)f) >> a.gshift);
+}
+// a / b where both mostly fit 32 bits
+__device__ __forceinline__ int64_t div64(int64_t x, int64_t y) {
+  return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
 
 // ---------------------------------------------------------------- the line of tiles
 struct Seq {
@@ -82,13 +102,14 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
 }
 __device__ __forceinline__ int unit_count(const Seq& s) { return (s.R + kUnit - 1) / kUnit; }
 // key tiles of unit qt: up to the position of its last row; one (masked) tile at least
-__device__ __forceinline__ int unit_tiles(const Seq& s, int G, int qt) {
-  const int tok = (min(s.R, (qt + 1) * kUnit) - 1) / G;
+__device__ __forceinline__ int unit_tiles(const Seq& s, const AttnArgs& a, int qt) {
+  const int tok = div_g(a, min(s.R, (qt + 1) * kUnit) - 1);
   const int64_t seen = min((int64_t)s.cap, (int64_t)s.len - s.T + tok + 1);
   return seen <= 0 ? 1 : (int)((seen + kTile - 1) / kTile);
 }
-// Tiles of one kv head of sequences b0 + lane (warp-wide call).
-__device__ int64_t head_tiles(const AttnArgs& a, int b, int lane) {
+// Cells of one kv head of sequence b (a lane each, warp-wide call). A unit
+// takes a cell more than its tiles: changing units costs about a tile's time.
+__device__ int64_t head_cells(const AttnArgs& a, int b, int lane) {
   Seq s{};
   int nq = 0;
   if (b < a.d.batch) {
@@ -97,7 +118,7 @@ __device__ int64_t head_tiles(const AttnArgs& a, int b, int lane) {
   }
   int64_t sum = 0;
   if (nq <= 4)
-    for (int i = 0; i < nq; ++i) sum += unit_tiles(s, a.G, i);
+    for (int i = 0; i < nq; ++i) sum += unit_tiles(s, a, i) + 1;
   unsigned big = __ballot_sync(CAS_FULL, nq > 4);
   while (big) {  // long chunks: the warp counts one together
     const int src = __ffs(big) - 1;
@@ -106,7 +127,7 @@ __device__ int64_t head_tiles(const AttnArgs& a, int b, int lane) {
     const Seq t = seq_of(a, bb);
     const int n = unit_count(t);
     int part = 0;
-    for (int i = lane; i < n; i += 32) part += unit_tiles(t, a.G, i);
+    for (int i = lane; i < n; i += 32) part += unit_tiles(t, a, i) + 1;
     part = warp_sum(part);
     if (lane == src) sum = part;
   }
@@ -114,32 +135,32 @@ __device__ int64_t head_tiles(const AttnArgs& a, int b, int lane) {
 }
 
 struct Place {
-  int b, hk, qt, tile;  // unit and its key tile
-  int64_t unit0;        // the unit's first tile on the line
+  int b, hk, qt, cell;  // unit and the cell inside it
 };
 struct Line {
-  int64_t total, per;  // tiles of all units, tiles a CTA takes
+  int64_t total, per;  // cells of all units, cells a CTA takes
 };
 
-// Warp-wide: the line's length, and the place of tile `c * per` on it (false
+// Warp-wide: the line's length, and the place of cell `c * per` on it (false
 // when the line is shorter).
 __device__ bool find_place(const AttnArgs& a, int64_t c, int grid, Line& line, Place& p) {
   const int lane = threadIdx.x & 31;
   int64_t total = 0, first = 0;
   for (int b0 = 0; b0 < a.d.batch; b0 += 32) {
-    int64_t t = head_tiles(a, b0 + lane, lane) * a.d.H;
+    int64_t t = head_cells(a, b0 + lane, lane);
     if (b0 == 0) first = t;
+    t *= a.d.H;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(CAS_FULL, t, d);
     total += t;
   }
   line.total = total;
-  line.per = max((int64_t)kMinTiles, (total + grid - 1) / grid);
+  line.per = max((int64_t)kMinCells, div64(total + grid - 1, grid));
   const int64_t want = c * line.per;
   if (want >= total) return false;
   int64_t base = 0;
   for (int b0 = 0; b0 < a.d.batch; b0 += 32) {
-    const int64_t t = b0 == 0 ? first : head_tiles(a, b0 + lane, lane) * a.d.H;
+    const int64_t h = b0 == 0 ? first : head_cells(a, b0 + lane, lane), t = h * a.d.H;
     int64_t incl = t;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -150,29 +171,23 @@ __device__ bool find_place(const AttnArgs& a, int64_t c, int grid, Line& line, P
     if (hit) {
       const int src = __ffs(hit) - 1;
       const int64_t before = base + __shfl_sync(CAS_FULL, incl - t, src);
-      const int64_t per_head = __shfl_sync(CAS_FULL, t, src) / a.d.H;
+      const int64_t per_head = __shfl_sync(CAS_FULL, h, src);
       p.b = b0 + src;
-      const int64_t rem = want - before;
-      p.hk = (int)(rem / per_head);
-      int64_t left = rem - p.hk * per_head;
-      p.unit0 = before + p.hk * per_head;
+      p.hk = (int)div64(want - before, per_head);
+      int64_t left = want - before - p.hk * per_head;
       const Seq s = seq_of(a, p.b);
       const int nq = unit_count(s);
       for (int q0 = 0; q0 < nq; q0 += 32) {
-        const int n = q0 + lane < nq ? unit_tiles(s, a.G, q0 + lane) : 0;
+        const int n = q0 + lane < nq ? unit_tiles(s, a, q0 + lane) + 1 : 0;
         const int up = warp_incl_add(n, lane);
         const unsigned in = __ballot_sync(CAS_FULL, up > left);
         if (in) {
           const int w = __ffs(in) - 1;
-          const int below = __shfl_sync(CAS_FULL, up - n, w);
           p.qt = q0 + w;
-          p.tile = (int)(left - below);
-          p.unit0 += below;
+          p.cell = (int)(left - __shfl_sync(CAS_FULL, up - n, w));
           return true;
         }
-        const int all = __shfl_sync(CAS_FULL, up, 31);
-        left -= all;
-        p.unit0 += all;
+        left -= __shfl_sync(CAS_FULL, up, 31);
       }
       return false;  // not reached: the unit lies in the sequence
     }
@@ -181,54 +196,27 @@ __device__ bool find_place(const AttnArgs& a, int64_t c, int grid, Line& line, P
   return false;
 }
 
-// The units of a CTA's piece of the line, walked by every warp in step.
-struct Walk {
-  int b, hk, qt;
-  int t0, n, all;  // first tile, tiles taken here, tiles of the unit
-  int64_t left;    // tiles of the piece from this unit on
-  Seq s;
-  bool first;
-  __device__ __forceinline__ void set(const AttnArgs& a) {
-    all = unit_tiles(s, a.G, qt);
-    n = (int)min((int64_t)(all - t0), left);
-  }
-  __device__ __forceinline__ void begin(const AttnArgs& a, const Place& p, int64_t tiles) {
-    b = p.b, hk = p.hk, qt = p.qt, t0 = p.tile, left = tiles, first = true;
-    s = seq_of(a, b);
-    set(a);
-  }
-  __device__ __forceinline__ bool next(const AttnArgs& a) {
-    left -= n;
-    if (left <= 0) return false;
-    first = false;
-    t0 = 0;
-    if (++qt >= unit_count(s)) {
-      qt = 0;
-      if (++hk >= a.d.H) {
-        hk = 0;
-        do {
-          if (++b >= a.d.batch) return false;
-          s = seq_of(a, b);
-        } while (s.R == 0);
-      }
-    }
-    set(a);
-    return true;
-  }
-  __device__ __forceinline__ int rows() const { return min(kUnit, s.R - qt * kUnit); }
-  __device__ __forceinline__ bool shared() const { return rows() > kTile; }  // both slots share the key tiles
+// A unit, or the part of it that a CTA takes.
+struct Unit {
+  int b, start, hk, f0, rows;  // sequence and its first row, kv head, flat rows
+  int pos0, kv_end;            // position of the sequence's first row, end of what it holds
+  int t0, n;                   // key tiles
+  int flags;                   // below
 };
+enum { kWhole = 1, kFirst = 2, kLast = 4, kNone = 8, kTileB = 16 };  // kTileB: Q in the second tile
 
 // ---------------------------------------------------------------- shared memory
 struct Aux {
-  uint64_t kv_full[kRing], kv_empty[kRing], q_full, s_full[2], p_full[2], o_full[2], drain;
+  uint64_t kv_full[kRing], kv_empty[kRing];
+  uint64_t u_full[2], u_empty[2], q_full[2], q_empty[2];
+  uint64_t s_full[2], p_full[2], o_full[2], merge, merged, drain;
   uint32_t tmem;
-  int abort, any;
-  Place place;
-  int64_t tiles;
+  int abort;
+  Unit unit[2];
+  float m[2][kTile], l[2][kTile];
 };
 
-__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t phase, volatile int* abort) {
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t phase, volatile int* abort) {
   for (uint32_t i = 0; i < kSpins; ++i) {
     if (mbar_try_wait(bar, phase)) return true;
     if ((i & 63) == 63 && *abort) return false;
@@ -237,216 +225,326 @@ __device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t phase, volatil
   atomicExch(&g_attn_status, CAS_ERR_TIMEOUT);
   return false;
 }
-// A wait that gave up marks the CTA; its threads then run through their loops
-// without waiting, computing or writing, so that all reach the end.
-__device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t phase, Aux* x, bool& dead) {
-  if (!dead && !mbar_try_wait(bar, phase)) dead = !wait_slow(bar, phase, &x->abort);
+// Warp-wide; false when any lane gave up.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t phase, Aux* x) {
+  bool ok = mbar_try_wait(bar, phase);
+  if (!__all_sync(CAS_FULL, ok)) ok = ok || wait_long(bar, phase, &x->abort);
+  return __all_sync(CAS_FULL, ok);
+}
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+// Unit number `u` of the CTA, read by a warp that then frees its place.
+__device__ __forceinline__ bool take_unit(uint32_t u, Aux* x, Unit& w) {
+  if (!wait(&x->u_full[u & 1], (u >> 1) & 1, x)) return false;
+  w = x->unit[u & 1];
+  arrive_warp(&x->u_empty[u & 1]);
+  return true;
 }
 
 // Ring position of K and V tile j of n: K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
 __device__ __forceinline__ uint32_t k_item(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ uint32_t v_item(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
 
-// ---------------------------------------------------------------- the roles
-__device__ void producer(const AttnArgs& a, const CUtensorMap* km, const CUtensorMap* vm, uint8_t* ring, Aux* x,
-                         const Place& place, int64_t tiles) {
+// ---------------------------------------------------------------- units and Q
+__device__ void scheduler(const AttnArgs& a, uint8_t* q_sm, Aux* x) {
+  const int lane = threadIdx.x & 31;
+  Line line;
+  Place p;
+  Unit w{};
+  Cut cut{};
+  const bool any = find_place(a, blockIdx.x, gridDim.x, line, p);
+  if (!any) {
+    if (lane == 0) {
+      a.cuts[blockIdx.x] = cut;
+      w.flags = kNone | kLast;
+      x->unit[0] = w;
+    }
+    arrive_warp(&x->u_full[0]);
+    return;
+  }
+  int64_t left = min(line.per, line.total - (int64_t)blockIdx.x * line.per);
+  Seq s = seq_of(a, p.b);
+  int cell = p.cell;
+  uint32_t uses[2] = {0, 0};  // of the Q tiles
+  for (uint32_t u = 0;; ++u) {
+    const int all = unit_tiles(s, a, p.qt);
+    const int end = (int)min((int64_t)all + 1, cell + left);
+    w.b = p.b, w.start = s.start, w.hk = p.hk, w.f0 = p.qt * kUnit;
+    w.rows = min(kUnit, s.R - w.f0);
+    w.pos0 = s.len - s.T;
+    w.kv_end = min(s.cap, s.len);
+    w.t0 = max(0, cell - 1);
+    w.n = max(0, end - 1) - w.t0;
+    left -= end - cell;
+    const bool two = w.rows > kTile, tile_b = !two && (u & 1);
+    w.flags = (w.n == all ? kWhole : 0) | (u == 0 ? kFirst : 0) | (tile_b ? kTileB : 0);
+    if (w.t0 == 0 && w.n > 0 && w.n < all) {  // the unit's first piece: its cut
+      cut.pieces = 1 + (int)div64(all - w.n + line.per - 1, line.per);
+      cut.start = w.start, cut.hk = w.hk, cut.f0 = w.f0, cut.rows = w.rows;
+      cut.first = u == 0 ? 0 : 1;
+    }
+    // the next unit, and whether it has a tile here (its first cell is none)
+    Seq s2 = s;
+    Place p2 = p;
+    if (++p2.qt >= unit_count(s)) {
+      p2.qt = 0;
+      if (++p2.hk >= a.d.H) {
+        p2.hk = 0;
+        do s2 = ++p2.b < a.d.batch ? seq_of(a, p2.b) : Seq{};
+        while (s2.R == 0 && p2.b < a.d.batch);
+      }
+    }
+    const bool last = left < 2 || p2.b >= a.d.batch;
+    if (last) w.flags |= kLast;
+    if (!wait(&x->u_empty[u & 1], ((u >> 1) & 1) ^ 1, x)) break;
+    if (lane == 0) x->unit[u & 1] = w;
+    arrive_warp(&x->u_full[u & 1]);
+    // Q: rows of 256 bytes into swizzled halves, 16 bytes a lane
+    const int first = tile_b ? 1 : 0, count = two ? 2 : 1;
+    bool ok = true;
+    for (int t = first; t < first + count; ++t) ok = ok && wait(&x->q_empty[t], (uses[t]++ & 1) ^ 1, x);
+    if (!ok) break;
+    const int c = lane & 15;
+#pragma unroll 4
+    for (int row = lane >> 4; row < count * kTile; row += 2) {
+      const int f = w.f0 + min(row, w.rows - 1), t = div_g(a, f), h = w.hk * a.G + (f - t * a.G);
+      const uint16_t* src = a.q + ((int64_t)(w.start + t) * a.Hq + h) * CAS_BLK + 8 * c;
+      const uint32_t dst = smem_u32(q_sm) + (first + (row >> 7)) * kBuf + (c >> 3) * kHalf + (row & 127) * 128 +
+                           (((c & 7) ^ (row & 7)) << 4);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(row < w.rows ? 16 : 0)
+                   : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_async_smem();
+    arrive_warp(&x->q_full[u & 1]);
+    if (last) break;
+    s = s2, p = p2, cell = 0;
+  }
+  if (lane == 0) a.cuts[blockIdx.x] = cut;
+}
+
+// ---------------------------------------------------------------- K and V
+// One warp loads K, another V: pages of 16 tokens take 16 boxes a tile, whose
+// issue would bound one warp.
+template <bool IS_V>
+__device__ void producer(const AttnArgs& a, const CUtensorMap* map, uint8_t* ring, Aux* x) {
   const int lane = threadIdx.x & 31;
   const int shift = min(a.d.shift, 7);  // log2 of tokens a box
   const int boxes = kTile >> shift;     // boxes a tile
-  uint32_t base = 0, issued = 0;
-  bool dead = false;
-  Walk w;
-  w.begin(a, place, tiles);
-  do {
-    // page and slot of this lane's box of tile j; pages past the last token and bad ids load zeros
-    const int seen = (int)min((int64_t)w.s.cap, (int64_t)w.s.len);
+  uint32_t base = 0;
+  uint32_t used = 0, phase = 0;  // buffers this warp has filled, and the phase of its newest copy
+  bool ok = true;
+  for (uint32_t u = 0; ok; ++u) {
+    Unit w;
+    if (!take_unit(u, x, w) || (w.flags & kNone)) break;
+    // page of this lane's box of tile j; pages past the last token and bad ids load zeros
     auto page_at = [&](int j) -> int {
       const int64_t tok = (int64_t)(w.t0 + j) * kTile + ((int64_t)lane << shift);
-      if (lane >= boxes || j >= w.n || tok >= seen) return -1;
-      return (int)page_of(a.d, w.b, tok);
+      if (lane >= boxes || j >= w.n || tok >= w.kv_end) return (int)a.d.n_pages;
+      const int64_t id = page_of(a.d, w.b, tok);
+      return id < 0 ? (int)a.d.n_pages : (int)id;
     };
-    auto load = [&](const CUtensorMap* map, uint32_t item, int j, int page) {
-      const uint32_t it = base + item, slot = it % kRing;
-      wait_or_die(&x->kv_empty[slot], ((it / kRing) & 1) ^ 1, x, dead);
-      dead = __any_sync(CAS_FULL, dead);
-      if (dead) return;
-      issued = it + 1;
+    int cur = page_at(0), nxt = page_at(1);
+    for (int j = 0; j < w.n; ++j) {
+      const uint32_t it = base + (IS_V ? v_item(j, w.n) : k_item(j)), slot = it % kRing;
+      ok = wait(&x->kv_empty[slot], ((it / kRing) & 1) ^ 1, x);
+      if (!ok) break;
+      used |= 1u << slot;
+      phase = (phase & ~(1u << slot)) | ((it / kRing) & 1) << slot;
       if (lane == 0) mbar_arrive_tx(&x->kv_full[slot], kBuf);
       __syncwarp();
       if (lane < boxes) {
         const int in_page = (int)(((int64_t)(w.t0 + j) * kTile + (lane << shift)) & ((1 << a.d.shift) - 1));
         uint8_t* dst = ring + slot * kBuf + ((uint32_t)lane << shift) * 128;
-        const int pg = page >= 0 ? page : (int)a.d.n_pages;
-        tma_load_4d(dst, map, 0, in_page, w.hk, pg, &x->kv_full[slot]);
-        tma_load_4d(dst + kHalf, map, 64, in_page, w.hk, pg, &x->kv_full[slot]);
+        tma_load_4d(dst, map, 0, in_page, w.hk, cur, &x->kv_full[slot]);
+        tma_load_4d(dst + kHalf, map, 64, in_page, w.hk, cur, &x->kv_full[slot]);
       }
-    };
-    int prev = -1, cur = page_at(0), nxt = page_at(1);
-    for (int j = 0; j < w.n; ++j) {
-      load(km, k_item(j), j, cur);
-      if (j > 0) load(vm, v_item(j - 1, w.n), j - 1, prev);
-      prev = cur;
       cur = nxt;
       nxt = page_at(j + 2);
     }
-    load(vm, v_item(w.n - 1, w.n), w.n - 1, prev);
     base += 2 * w.n;
-  } while (w.next(a));
-  if (dead)  // copies in flight land before the block ends
-    for (uint32_t it = issued > kRing ? issued - kRing : 0; it < issued; ++it)
-      mbar_wait_bounded(&x->kv_full[it % kRing], (it / kRing) & 1, kSpins);
+    if (w.flags & kLast) break;
+  }
+  // after a wait that gave up, copies in flight land before the block ends
+  if (*(volatile int*)&x->abort)
+    for (int i = 0; i < kRing; ++i)
+      if (used >> i & 1) mbar_wait_bounded(&x->kv_full[i], phase >> i & 1, kSpins);
 }
 
-__device__ void issuer(const AttnArgs& a, uint32_t q_sm, uint32_t ring_sm, Aux* x, const Place& place, int64_t tiles) {
-  const uint32_t tm = x->tmem;
+// ---------------------------------------------------------------- products
+__device__ void issuer(uint32_t q_sm, uint32_t ring_sm, Aux* x) {
+  const uint32_t tm = __reduce_max_sync(CAS_FULL, x->tmem);
   constexpr uint32_t id_s = tc_idesc_bf16(kTile, kTile, false), id_o = tc_idesc_bf16(kTile, CAS_BLK, true);
-  uint32_t base = 0, np[2] = {0, 0}, unit = 0;
-  bool dead = false;
+  uint32_t base = 0, np[2] = {0, 0};
+  bool ok = true;
   auto wait_kv = [&](uint32_t item) {
     const uint32_t it = base + item;
-    wait_or_die(&x->kv_full[it % kRing], (it / kRing) & 1, x, dead);
+    ok = ok && wait(&x->kv_full[it % kRing], (it / kRing) & 1, x);
   };
   auto free_kv = [&](uint32_t item) {
-    if (!dead) tc_commit(&x->kv_empty[(base + item) % kRing]);
+    if (ok && elect_one()) tc_commit(&x->kv_empty[(base + item) % kRing]);
   };
-  auto mma_s = [&](int slot, uint32_t q_tile, uint32_t item) {
-    if (dead) return;
-    const uint32_t kb = ring_sm + ((base + item) % kRing) * kBuf, qb = q_sm + q_tile * kBuf;
+  auto signal = [&](uint64_t* bar) {
+    if (ok && elect_one()) tc_commit(bar);
+  };
+  auto mma_s = [&](int slot, uint32_t tile, uint32_t item) {
+    const uint32_t buf = __shfl_sync(CAS_FULL, (base + item) % kRing, 0);
     tc_fence_after();
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
-      tc_mma_ss(tm + slot * kTile, tc_desc(qb + off, 16, 1024), tc_desc(kb + off, 16, 1024), id_s, k > 0);
+    if (ok && elect_one()) {
+      tc_product_ss(tm + slot * kTile, tc_desc_lo(q_sm + tile * kBuf, 16), tc_desc_lo(ring_sm + buf * kBuf, 16), id_s);
+      tc_commit(&x->s_full[slot]);
     }
-    tc_commit(&x->s_full[slot]);
   };
   auto mma_o = [&](int slot, uint32_t item, bool add) {
-    if (dead) return;
-    const uint32_t vb = ring_sm + ((base + item) % kRing) * kBuf;
+    const uint32_t buf = __shfl_sync(CAS_FULL, (base + item) % kRing, 0);
     tc_fence_after();
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      tc_mma_ts(tm + 2 * kTile + slot * CAS_BLK, tm + slot * kTile + 8 * k, tc_desc(vb + k * 2048, kHalf, 1024), id_o,
-                add || k > 0);
+    if (ok && elect_one())
+      tc_product_ts(tm + 2 * kTile + slot * CAS_BLK, tm + slot * kTile, tc_desc_lo(ring_sm + buf * kBuf, kHalf), id_o,
+                    add);
   };
-  auto wait_p = [&](int slot) { wait_or_die(&x->p_full[slot], np[slot]++ & 1, x, dead); };
-  Walk w;
-  w.begin(a, place, tiles);
-  do {
-    wait_or_die(&x->q_full, unit++ & 1, x, dead);
+  auto wait_p = [&](int slot) { ok = ok && wait(&x->p_full[slot], np[slot]++ & 1, x); };
+  for (uint32_t u = 0; ok; ++u) {
+    Unit w;
+    if (!take_unit(u, x, w) || (w.flags & kNone)) break;
+    ok = wait(&x->q_full[u & 1], (u >> 1) & 1, x);
     const int n = w.n;
-    if (w.shared()) {
+    if (w.rows > kTile) {
       wait_kv(k_item(0));
       mma_s(0, 0, k_item(0));
       mma_s(1, 1, k_item(0));
       free_kv(k_item(0));
-      for (int j = 0; j < n; ++j) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          wait_p(i);
-          if (i == 0) wait_kv(v_item(j, n));
-          mma_o(i, v_item(j, n), j > 0);
-          if (i == 1) free_kv(v_item(j, n));
-          if (j + 1 < n) {
-            if (i == 0) wait_kv(k_item(j + 1));
-            mma_s(i, i, k_item(j + 1));
-            if (i == 1) free_kv(k_item(j + 1));
-          } else if (!dead) {
-            tc_commit(&x->o_full[i]);
-          }
+      if (n == 1) signal(&x->q_empty[0]), signal(&x->q_empty[1]);
+      for (int j = 0; j < n && ok; ++j) {
+        const uint32_t v = v_item(j, n), k = k_item(j + 1);
+        const bool more = j + 1 < n;
+        wait_p(0);
+        wait_kv(v);
+        mma_o(0, v, j > 0);
+        if (more) {
+          wait_kv(k);
+          mma_s(0, 0, k);
+          if (j + 2 == n) signal(&x->q_empty[0]);
+        } else {
+          signal(&x->o_full[0]);
+        }
+        wait_p(1);
+        mma_o(1, v, j > 0);
+        free_kv(v);
+        if (more) {
+          mma_s(1, 1, k);
+          free_kv(k);
+          if (j + 2 == n) signal(&x->q_empty[1]);
+        } else {
+          signal(&x->o_full[1]);
         }
       }
     } else {
+      const int t = (w.flags & kTileB) ? 1 : 0;
       for (int j = 0; j < min(n, 2); ++j) {
         wait_kv(k_item(j));
-        mma_s(j, 0, k_item(j));
+        mma_s(j, t, k_item(j));
         free_kv(k_item(j));
+        if (j + 1 == n) signal(&x->q_empty[t]);
       }
-      for (int j = 0; j < n; ++j) {
+      for (int j = 0; j < n && ok; ++j) {
         const int i = j & 1;
+        const uint32_t v = v_item(j, n), k = k_item(j + 2);
         wait_p(i);
-        wait_kv(v_item(j, n));
-        mma_o(i, v_item(j, n), j >= 2);
-        free_kv(v_item(j, n));
+        wait_kv(v);
+        mma_o(i, v, j >= 2);
+        free_kv(v);
         if (j + 2 < n) {
-          wait_kv(k_item(j + 2));
-          mma_s(i, 0, k_item(j + 2));
-          free_kv(k_item(j + 2));
-        } else if (!dead) {
-          tc_commit(&x->o_full[i]);
+          wait_kv(k);
+          mma_s(i, t, k);
+          free_kv(k);
+          if (j + 3 == n) signal(&x->q_empty[t]);
+        } else {
+          signal(&x->o_full[i]);
         }
       }
     }
     base += 2 * n;
-  } while (w.next(a));
-  tc_commit(&x->drain);  // products in flight end before the block does
+    if (w.flags & kLast) break;
+  }
+  if (elect_one()) tc_commit(&x->drain);  // products in flight end before the block does
+  __syncwarp();
   mbar_wait_bounded(&x->drain, 0, kSpins);
 }
 
+// ---------------------------------------------------------------- softmax
 // Scale of the scores in powers of two: log2(e) / sqrt(128).
 constexpr float kScaleLog2 = 0.08838834764831845f * 1.4426950408889634f;
 
-__device__ void softmax(const AttnArgs& a, uint8_t* q_sm, uint8_t* ring, Aux* x, const Place& place, int64_t tiles) {
+__device__ __forceinline__ void store32(void* p, const uint32_t* v, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+__device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
   const int slot = threadIdx.x >> 7, r = threadIdx.x & 127, warp = r >> 5;
   const uint32_t tm = x->tmem + ((uint32_t)warp << 21);
   const uint32_t tm_s = tm + slot * kTile, tm_o = tm + 2 * kTile + slot * CAS_BLK;
-  uint32_t base = 0, ns = 0, no = 0;
-  bool dead = false;
-  Walk w;
-  w.begin(a, place, tiles);
-  do {
-    const bool two = w.shared();
-    const int rows = w.rows();
-    const int f0 = w.qt * kUnit;
-    // Q: rows of 256 bytes into swizzled halves; both warpgroups load the unit's rows
-    {
-      const int nrow = two ? kUnit : kTile;
-      for (int i = threadIdx.x; i < nrow * 16; i += 256) {
-        const int row = i >> 4, c = i & 15;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < rows) {
-          const int f = f0 + row, t = f / a.G, h = w.hk * a.G + (f - t * a.G);
-          v = __ldg(reinterpret_cast<const uint4*>(a.q + ((int64_t)(w.s.start + t) * a.Hq + h) * CAS_BLK) + c);
-        }
-        *reinterpret_cast<uint4*>(q_sm + (row >> 7) * kBuf + (c >> 3) * kHalf + (row & 127) * 128 +
-                                  (((c & 7) ^ (row & 7)) << 4)) = v;
-      }
-      fence_async_smem();
-      mbar_arrive(&x->q_full);
-    }
-    // this thread's row: the last position it sees
-    const int fr = two ? slot * kTile + r : r;  // row in the unit
-    const bool mine = fr < rows;
-    const int f = f0 + fr;
-    const int64_t seen = min((int64_t)w.s.cap, (int64_t)w.s.len - w.s.T + (mine ? f / a.G : w.s.T - 1) + 1);
-    const int lim = (int)max((int64_t)0, seen) - 1;  // -1: sees nothing
+  uint32_t base = 0, ns = 0, no = 0, nm = 0;
+  bool pending = false;  // the other slot may still read this slot's O
+  for (uint32_t u = 0;; ++u) {
+    Unit w;
+    if (!take_unit(u, x, w) || (w.flags & kNone)) return;
+    const bool two = w.rows > kTile;  // both slots share the key tiles
+    // this thread's row: the last position it sees (-1: none)
+    const int fr = two ? slot * kTile + r : r;
+    const bool mine = fr < w.rows;
+    const int f = w.f0 + (mine ? fr : w.rows - 1), tok = div_g(a, f);
+    const int lim = max(0, min(w.kv_end, w.pos0 + tok + 1)) - 1;
     const bool busy = __any_sync(CAS_FULL, mine);
-    const int kv_end = (int)min((int64_t)w.s.cap, (int64_t)w.s.len);
     float m = -INFINITY, l = 0.f;
     int done = 0;
-    const int j0 = two ? 0 : slot, step = two ? 1 : 2;
-    for (int j = j0; j < w.n; j += step) {
+    const int step = two ? 1 : 2;
+    for (int j = two ? 0 : slot; j < w.n; j += step) {
       const int key0 = (w.t0 + j) * kTile;
-      wait_or_die(&x->s_full[slot], ns++ & 1, x, dead);
+      if (!wait(&x->s_full[slot], ns++ & 1, x)) return;
       tc_fence_after();
-      if (busy && !dead) {
+      if (busy) {
         uint32_t s[kTile];
+        tm_ld32(s, tm_s);
+        tm_ld32(s + 32, tm_s + 32);
+        tm_wait_ld(s);
+        tm_wait_ld(s + 32);
+        tm_ld32(s + 64, tm_s + 64);
+        tm_ld32(s + 96, tm_s + 96);
+        const bool edge = __any_sync(CAS_FULL, key0 + kTile - 1 > lim);
+        const int last = lim - key0;
+        if (edge) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tm_ld32(s + 32 * c, tm_s + 32 * c);
-        tm_wait_ld();
-        if (__any_sync(CAS_FULL, key0 + kTile - 1 > lim)) {
-          const int last = lim - key0;
-#pragma unroll
-          for (int c = 0; c < kTile; ++c)
+          for (int c = 0; c < 64; ++c)
             if (c > last) s[c] = 0xFF800000u;
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < kTile; c += 8)
+        for (int c = 0; c < 64; c += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(s[c + k])), __uint_as_float(s[c + 4 + k]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kScaleLog2;
+            mx[k] = max3(mx[k], __uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1]));
+        tm_wait_ld(s + 64);
+        tm_wait_ld(s + 96);
+        if (edge) {
+#pragma unroll
+          for (int c = 64; c < kTile; ++c)
+            if (c > last) s[c] = 0xFF800000u;
+        }
+#pragma unroll
+        for (int c = 64; c < kTile; c += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx[k] = max3(mx[k], __uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1]));
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * kScaleLog2;
         const bool grow = top > m + 8.f;
         if (done == 0) {
           m = top;
@@ -455,40 +553,45 @@ __device__ void softmax(const AttnArgs& a, uint8_t* q_sm, uint8_t* ring, Aux* x,
           const float fac = grow ? ex2(m - top) : 1.f;
           if (grow) m = top;
           l *= fac;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t v[32];
             tm_ld32(v, tm_o + 32 * c);
-            tm_wait_ld();
+            tm_wait_ld(v);
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * fac);
             tm_st32(tm_o + 32 * c, v);
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t sc2 = pack2(kScaleLog2, kScaleLog2), ref2 = pack2(-ref, -ref);
+        uint64_t ls[2] = {0, 0};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t p[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            const float e0 = ex2(fmaf(__uint_as_float(s[64 * c + 2 * k]), kScaleLog2, -ref));
-            const float e1 = ex2(fmaf(__uint_as_float(s[64 * c + 2 * k + 1]), kScaleLog2, -ref));
-            ls[k & 1] += e0;
-            ls[2 + (k & 1)] += e1;
+            float e0, e1;
+            unpack2(fma2(pack2(__uint_as_float(s[64 * c + 2 * k]), __uint_as_float(s[64 * c + 2 * k + 1])), sc2, ref2), e0,
+                    e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            ls[k & 1] = add2(ls[k & 1], pack2(e0, e1));
             p[k] = pack_bf16x2(e0, e1);
           }
           tm_st32(tm_s + 32 * c, p);
         }
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        float l0, l1;
+        unpack2(add2(ls[0], ls[1]), l0, l1);
+        l += l0 + l1;
         tm_wait_st();
       }
       ++done;
-      if (key0 + kTile > kv_end && (slot == 0 || !two)) {
+      if (key0 + kTile > w.kv_end && (slot == 0 || !two)) {
         // slots behind the last token may hold anything: their V rows become zeros
         const uint32_t it = base + v_item(j, w.n);
-        wait_or_die(&x->kv_full[it % kRing], (it / kRing) & 1, x, dead);
-        if (key0 + r >= kv_end && !dead) {
+        if (!wait(&x->kv_full[it % kRing], (it / kRing) & 1, x)) return;
+        if (key0 + r >= w.kv_end) {
           uint4* row = reinterpret_cast<uint4*>(ring + (it % kRing) * kBuf + r * 128);
 #pragma unroll
           for (int c = 0; c < 8; ++c) row[c] = row[kHalf / 16 + c] = make_uint4(0, 0, 0, 0);
@@ -496,138 +599,142 @@ __device__ void softmax(const AttnArgs& a, uint8_t* q_sm, uint8_t* ring, Aux* x,
         fence_async_smem();
       }
       tc_fence_before();
-      mbar_arrive(&x->p_full[slot]);
+      if (pending) {
+        if (!wait(&x->merged, (nm - 1) & 1, x)) return;
+        pending = false;
+      }
+      arrive_warp(&x->p_full[slot]);
     }
     base += 2 * w.n;
     // ---- epilogue
+    if (pending) {  // (no tile was this slot's)
+      if (!wait(&x->merged, (nm - 1) & 1, x)) return;
+      pending = false;
+    }
     if (done > 0) {
-      wait_or_die(&x->o_full[slot], no++ & 1, x, dead);
+      if (!wait(&x->o_full[slot], no++ & 1, x)) return;
       tc_fence_after();
     }
     float w0 = 1.f, w1 = 0.f;  // weights of the two slots' outputs
     int c0 = 0, c1 = 4;        // 32-column chunks that this thread writes
     if (!two) {
-      float* ml = reinterpret_cast<float*>(q_sm + kBuf);  // the second Q tile is not used here
-      ml[slot * kTile + r] = m;
-      ml[(2 + slot) * kTile + r] = l;
+      x->m[slot][r] = m;
+      x->l[slot][r] = l;
       tc_fence_before();
-      named_sync(1, 256);
+      arrive_warp(&x->merge);
+      if (!wait(&x->merge, nm & 1, x)) return;
       tc_fence_after();
-      const float ma = ml[r], mb = ml[kTile + r];
-      const float top = fmaxf(ma, mb), ref = top == -INFINITY ? 0.f : top;
-      w0 = ex2(ma - ref);
-      w1 = w.n > 1 ? ex2(mb - ref) : 0.f;
-      l = ml[2 * kTile + r] * w0 + (w.n > 1 ? ml[3 * kTile + r] * w1 : 0.f);
+      const bool other = w.n > 1;  // slot 1 had tiles
+      const float mb = other ? x->m[1][r] : -INFINITY;
+      const float top = fmaxf(x->m[0][r], mb), ref = top == -INFINITY ? 0.f : top;
+      w0 = ex2(x->m[0][r] - ref);
+      w1 = ex2(mb - ref);
+      l = x->l[0][r] * w0 + (other ? x->l[1][r] * w1 : 0.f);
       m = top;
       c0 = 2 * slot;
       c1 = c0 + 2;
     }
-    if (busy && !dead) {
-      const bool whole = w.n == w.all;
+    if (busy) {
+      const bool whole = w.flags & kWhole;
       const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
-      const int t = f / a.G, h = w.hk * a.G + (f - t * a.G);
-      uint16_t* out = a.o + ((int64_t)(w.s.start + t) * a.Hq + h) * CAS_BLK;
-      float* part = a.ws + ((int64_t)(2 * blockIdx.x + (w.first ? 0 : 1)) * a.piece_rows + fr) * kPieceFloats;
+      float* part = a.ws + (int64_t)(2 * blockIdx.x + (w.flags & kFirst ? 0 : 1)) * a.piece_rows * kPieceFloats;
+      uint16_t* out = a.o + ((int64_t)(w.start + tok) * a.Hq + w.hk * a.G + (f - tok * a.G)) * CAS_BLK;
       const uint32_t o0 = two ? tm_o : tm + 2 * kTile;
+#pragma unroll 1
       for (int c = c0; c < c1; ++c) {
         uint32_t v[32];
         tm_ld32(v, o0 + 32 * c);
-        tm_wait_ld();
-        if (!two) {
-          if (w.n > 1) {
-            uint32_t u[32];
-            tm_ld32(u, o0 + CAS_BLK + 32 * c);
-            tm_wait_ld();
+        tm_wait_ld(v);
+        if (!two && w.n > 1) {
+          uint32_t t[32];
+          tm_ld32(t, o0 + CAS_BLK + 32 * c);
+          tm_wait_ld(t);
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              v[k] = __float_as_uint(__uint_as_float(v[k]) * w0 + __uint_as_float(u[k]) * w1);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * w0);
-          }
+          for (int k = 0; k < 32; ++k)
+            v[k] = __float_as_uint(__uint_as_float(v[k]) * w0 + __uint_as_float(t[k]) * w1);
         }
         if (!mine) continue;
         if (whole) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint4 q;
-            q.x = pack_bf16x2(__uint_as_float(v[8 * k]) * inv, __uint_as_float(v[8 * k + 1]) * inv);
-            q.y = pack_bf16x2(__uint_as_float(v[8 * k + 2]) * inv, __uint_as_float(v[8 * k + 3]) * inv);
-            q.z = pack_bf16x2(__uint_as_float(v[8 * k + 4]) * inv, __uint_as_float(v[8 * k + 5]) * inv);
-            q.w = pack_bf16x2(__uint_as_float(v[8 * k + 6]) * inv, __uint_as_float(v[8 * k + 7]) * inv);
-            *reinterpret_cast<uint4*>(out + 32 * c + 8 * k) = q;
-          }
+          for (int k = 0; k < 16; ++k)
+            v[k] = pack_bf16x2(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv);
+          store32(out + 32 * c, v, a.wide);
+          store32(out + 32 * c + 16, v + 8, a.wide);
         } else {
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            *reinterpret_cast<float2*>(part + 32 * c + 2 * k) =
-                make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
-          if (c == 0) *reinterpret_cast<float2*>(part + CAS_BLK) = make_float2(m, l);
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(part + ((int64_t)(8 * c + k) * a.piece_rows + fr) * 4) =
+                make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          if (c == 0) {
+            part[(int64_t)CAS_BLK * a.piece_rows + fr] = m;
+            part[(int64_t)(CAS_BLK + 1) * a.piece_rows + fr] = l;
+          }
         }
       }
     }
     tc_fence_before();
-    // O of both slots, and the rows' m and l, are read before the next unit writes them;
-    // Q is free too: both slots' scores are complete
-    named_sync(2, 256);
-    tc_fence_after();
-  } while (w.next(a));
+    if (!two) {  // both slots' O, m and l are read before either is written again
+      arrive_warp(&x->merged);
+      ++nm;
+      pending = true;
+    }
+    if (w.flags & kLast) return;
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap km,
                       const __grid_constant__ CUtensorMap vm) {
-  extern __shared__ uint8_t raw[];
-  uint8_t* base = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
-  uint8_t* q_sm = base;
-  uint8_t* ring = base + 2 * kBuf;
+  extern __shared__ __align__(1024) uint8_t q_sm[];
+  uint8_t* ring = q_sm + 2 * kBuf;
   Aux* x = reinterpret_cast<Aux*>(ring + kRing * kBuf);
   const int warp = threadIdx.x >> 5;
+  if (smem_u32(q_sm) & 1023) {  // swizzled tiles need it; dynamic shared memory starts there
+    if (threadIdx.x == 0) atomicExch(&g_attn_status, CAS_ERR_CUDA);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&x->kv_full[i], 1);
       mbar_init(&x->kv_empty[i], 1);
     }
-    mbar_init(&x->q_full, 256);
-    mbar_init(&x->drain, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&x->u_full[i], 1);
+      mbar_init(&x->u_empty[i], 11);  // eight softmax warps, two producers, the issuer
+      mbar_init(&x->q_full[i], 1);
+      mbar_init(&x->q_empty[i], 1);
       mbar_init(&x->s_full[i], 1);
-      mbar_init(&x->p_full[i], kTile);
+      mbar_init(&x->p_full[i], 4);
       mbar_init(&x->o_full[i], 1);
     }
+    mbar_init(&x->merge, 8);
+    mbar_init(&x->merged, 8);
+    mbar_init(&x->drain, 1);
     x->abort = 0;
     fence_mbar_init();
     fence_async_smem();
   }
+  if (warp == 8) tma_prefetch_map(&km);
+  if (warp == 10) tma_prefetch_map(&vm);
   if (warp == 9) tm_alloc(&x->tmem, 512);
-  pdl_wait();
-  pdl_trigger();
-  if (warp == 0) {
-    Line line;
-    Place p;
-    const bool any = find_place(a, blockIdx.x, gridDim.x, line, p);
-    if (threadIdx.x == 0) {
-      x->any = any;
-      x->place = p;
-      x->tiles = any ? min(line.per, line.total - (int64_t)blockIdx.x * line.per) : 0;
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (x->any) {
-    const Place p = x->place;
-    const int64_t tiles = x->tiles;
-    if (warp < 8) {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-      softmax(a, q_sm, ring, x, p, tiles);
-    } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-      if (warp == 8)
-        producer(a, &km, &vm, ring, x, p, tiles);
-      else if (threadIdx.x == 9 * 32)
-        issuer(a, smem_u32(q_sm), smem_u32(ring), x, p, tiles);
-    }
+  pdl_wait();
+  pdl_trigger();
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    softmax(a, ring, x);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == 8)
+      producer<false>(a, &km, ring, x);
+    else if (warp == 10)
+      producer<true>(a, &vm, ring, x);
+    else if (warp == 9)
+      issuer(smem_u32(q_sm), smem_u32(ring), x);
+    else
+      scheduler(a, q_sm, x);
   }
   __syncwarp();
   tc_fence_before();
@@ -635,63 +742,71 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   if (warp == 9) tm_free(x->tmem, 512);
 }
-constexpr size_t kSmem = 1024 + (2 + kRing) * (size_t)kBuf + sizeof(Aux);
+constexpr size_t kSmem = (2 + kRing) * (size_t)kBuf + sizeof(Aux);
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
 // ---------------------------------------------------------------- joining the pieces
-// Block (c, y) looks at the cut between CTA c and c + 1: if it is the first cut
-// inside a unit, it merges the unit's pieces for rows 32 y to 32 y + 31.
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs a, int grid) {
-  __shared__ Place sp;
-  __shared__ Line sl;
-  __shared__ int any;
-  // row_start and kv_len are older than the attention kernel, whose start this kernel's start follows
-  if (threadIdx.x < 32) {
-    Line line;
-    Place p;
-    const bool ok = find_place(a, blockIdx.x + 1, grid, line, p);
-    if (threadIdx.x == 0) sp = p, sl = line, any = ok;
+// Block (c, y) merges a part of the pieces of the unit whose first cut lies
+// behind CTA c: 16 of the 128 values of its rows. An item is 4 values of a row,
+// neighbouring threads take neighbouring rows; where there are fewer items than
+// threads, several threads share an item's pieces, so that all loads are in
+// flight together.
+constexpr int kJoinThreads = 256, kJoinSplit = 8;
+struct Part {
+  float m, l;
+  float4 o;
+  __device__ __forceinline__ void add(float pm, float pl, float4 v) {
+    const float top = fmaxf(m, pm), ref = top == -INFINITY ? 0.f : top;
+    const float f = ex2(m - ref), g = ex2(pm - ref);
+    m = top;
+    l = l * f + pl * g;
+    o.x = o.x * f + v.x * g;
+    o.y = o.y * f + v.y * g;
+    o.z = o.z * f + v.z * g;
+    o.w = o.w * f + v.w * g;
   }
+};
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs a) {
+  __shared__ Part sp[kJoinThreads];
   pdl_wait();
   pdl_trigger();
-  __syncthreads();
-  if (!any) return;
-  const Place p = sp;
-  const int64_t per = sl.per;
-  if (p.tile == 0 || (int64_t)blockIdx.x * per > p.unit0) return;  // no cut, or not the unit's first
-  const Seq s = seq_of(a, p.b);
-  const int64_t end = p.unit0 + unit_tiles(s, a.G, p.qt);
-  const int c0 = blockIdx.x, c1 = (int)((end - 1) / per);
-  const int rows = min(kUnit, s.R - p.qt * kUnit), lane = threadIdx.x & 31;
-  for (int i = 0; i < 4; ++i) {
-    const int fr = blockIdx.y * 32 + (threadIdx.x >> 5) * 4 + i;
-    if (fr >= rows) return;
-    // CTA c0 met the unit as its first one only if its piece starts with it
-    auto piece = [&](int c) {
-      const int which = (int64_t)c * per >= p.unit0 ? 0 : 1;
-      return a.ws + ((int64_t)(2 * c + which) * a.piece_rows + fr) * kPieceFloats;
-    };
-    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int c = c0; c <= c1; ++c) {
-      const float* w = piece(c);
-      const float pm = w[CAS_BLK], pl = w[CAS_BLK + 1];
-      const float2 v0 = *reinterpret_cast<const float2*>(w + 4 * lane);
-      const float2 v1 = *reinterpret_cast<const float2*>(w + 4 * lane + 2);
-      const float top = fmaxf(m, pm), ref = top == -INFINITY ? 0.f : top;
-      const float f = ex2(m - ref), g = ex2(pm - ref);
-      l = l * f + pl * g;
-      acc[0] = acc[0] * f + v0.x * g;
-      acc[1] = acc[1] * f + v0.y * g;
-      acc[2] = acc[2] * f + v1.x * g;
-      acc[3] = acc[3] * f + v1.y * g;
-      m = top;
+  const Cut cut = a.cuts[blockIdx.x];
+  if (cut.pieces < 2) return;
+  const int items = cut.rows * (32 / kJoinSplit);
+  int width = 4;  // threads side by side on items: a power of two
+  while (width < items && width < kJoinThreads) width *= 2;
+  const int share = kJoinThreads / width, mine = threadIdx.x & (width - 1), sub = threadIdx.x / width;
+  const int64_t size = (int64_t)a.piece_rows * kPieceFloats, half = (int64_t)CAS_BLK * a.piece_rows;
+  const float* base = a.ws + (int64_t)2 * blockIdx.x * size;
+  for (int i0 = 0; i0 < items; i0 += width) {
+    const int i = i0 + mine, q = i / cut.rows, fr = i - q * cut.rows, c = blockIdx.y * (32 / kJoinSplit) + q;
+    Part p{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (i < items) {
+#pragma unroll 4
+      for (int k = sub; k < cut.pieces; k += share) {
+        // the unit is the first of every CTA but, perhaps, the first one
+        const float* w = base + (k == 0 ? cut.first : 2 * k) * size;
+        p.add(w[half + fr], w[half + a.piece_rows + fr],
+              *reinterpret_cast<const float4*>(w + ((int64_t)c * a.piece_rows + fr) * 4));
+      }
     }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    const int f = p.qt * kUnit + fr, t = f / a.G, h = p.hk * a.G + (f - t * a.G);
-    uint2 out;
-    out.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    out.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-    *reinterpret_cast<uint2*>(a.o + ((int64_t)(s.start + t) * a.Hq + h) * CAS_BLK + 4 * lane) = out;
+    if (share > 1) {
+      sp[threadIdx.x] = p;
+      __syncthreads();
+      if (sub == 0)
+        for (int k = 1; k < share; ++k) {
+          const Part& t = sp[k * width + mine];
+          p.add(t.m, t.l, t.o);
+        }
+    }
+    if (sub == 0 && i < items) {
+      const float inv = p.l > 0.f || p.l != p.l ? 1.f / p.l : 0.f;
+      const int f = cut.f0 + fr, t = div_g(a, f), h = cut.hk * a.G + (f - t * a.G);
+      uint2 out;
+      out.x = pack_bf16x2(p.o.x * inv, p.o.y * inv);
+      out.y = pack_bf16x2(p.o.z * inv, p.o.w * inv);
+      *reinterpret_cast<uint2*>(a.o + ((int64_t)(cut.start + t) * a.Hq + h) * CAS_BLK + 4 * c) = out;
+    }
   }
 }
 
@@ -747,7 +862,8 @@ int attn_wait_status(bool clear) {
 using namespace cas;
 
 extern "C" uint64_t cas_paged_attn_workspace_bytes(int rows, int n_q_heads, int n_kv_heads) {
-  return (uint64_t)2 * sm_count() * piece_rows(rows, n_q_heads, n_kv_heads) * kPieceFloats * 4;
+  const int64_t g = sm_count();
+  return ((uint64_t)g * sizeof(Cut) + 255) / 256 * 256 + 2 * g * piece_rows(rows, n_q_heads, n_kv_heads) * kPieceFloats * 4;
 }
 
 extern "C" int cas_paged_attn(const cas_paged_kv* kv, const cas_paged_batch* b, const uint16_t* q, int n_q_heads,
@@ -765,17 +881,21 @@ extern "C" int cas_paged_attn(const cas_paged_kv* kv, const cas_paged_batch* b, 
   a.d = make_paged_dev(kv, b);
   a.q = q;
   a.o = o;
-  a.ws = (float*)workspace;
+  const int grid = sm_count();
+  a.cuts = (Cut*)workspace;
+  a.ws = (float*)((uint8_t*)workspace + ((size_t)grid * sizeof(Cut) + 255) / 256 * 256);
   a.Hq = n_q_heads;
+  a.wide = ((uintptr_t)o & 31) == 0;
   a.G = n_q_heads / kv->n_kv_heads;
   a.piece_rows = piece_rows(b->rows, n_q_heads, kv->n_kv_heads);
+  while ((1 << a.gshift) < a.G) ++a.gshift;
+  a.gmul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << a.gshift) - a.G)) / a.G + 1);
   CUtensorMap km, vm;
   if (!make_map(&km, kv, kv->k) || !make_map(&vm, kv, kv->v)) return CAS_ERR_CUDA;
   if (occupancy((const void*)paged_attn_kernel, kThreads, kSmem) < 1) return CAS_ERR_CUDA;
-  const int grid = sm_count();
   const cudaStream_t st = (cudaStream_t)stream;
   if (const int e = launch_k(paged_attn_kernel, grid, kThreads, kSmem, st, a, km, vm)) return e;
   if (grid < 2) return CAS_OK;
   // directly behind our own kernel: its launch may overlap that kernel's tail
-  return launch_with(true, attn_join_kernel, dim3(grid - 1, (a.piece_rows + 31) / 32), 256, 0, st, a, grid);
+  return launch_with(true, attn_join_kernel, dim3(grid - 1, kJoinSplit), kJoinThreads, 0, st, a);
 }

@@ -44,7 +44,7 @@ struct SpecArgs {
   int batch, gamma, slices;
   int64_t vecs;  // 16-byte groups a slice
   double temp;
-  float c;       // log2(e) / T
+  float c, c_lo;  // log2(e) / T as two floats
   int32_t *n_accepted, *tokens;
   float* ratio;
   float2* part;  // [batch][2 gamma + 1][slices]: maximum and sum, or maximum and its index
@@ -252,10 +252,24 @@ __device__ __forceinline__ uint64_t weight(float l, const Weigh& w, Scale c) {
   return sh >= 0 ? (uint64_t)full << sh : sh > -64 ? (uint64_t)full >> -sh : 0ull;
 }
 
+// 2^(j / 32)
+__constant__ double kPow2[32] = {
+    1.0, 1.0218971486541166, 1.0442737824274138, 1.0671404006768237,
+    1.0905077326652577, 1.1143867425958924, 1.1387886347566916, 1.1637248587775775,
+    1.189207115002721, 1.215247359980469, 1.241857812073484, 1.2690509571917332,
+    1.2968395546510096, 1.3252366431597413, 1.3542555469368927, 1.383909881963832,
+    1.4142135623730951, 1.4451808069770467, 1.4768261459394993, 1.5091644275934228,
+    1.5422108254079407, 1.5759808451078865, 1.6104903319492543, 1.645755478153965,
+    1.681792830507429, 1.718619298122478, 1.7562521603732995, 1.7947090750031072,
+    1.8340080864093424, 1.8741676341103, 1.9152065613971474, 1.9571441241754002};
+
 struct Shared {
   float M[2 * kMaxGamma + 1], Z[2 * kMaxGamma + 1];
   float ratio[kMaxGamma];
   float2 table[3][32];  // plain, target / sum, draft / sum
+  Weigh w[4];           // target, draft; the same over their sums
+  double factor[2];
+  uint64_t goal;
   uint64_t warp[2][kThreads / 32];
   uint64_t sum[2];      // this CTA's share of the target's and the draft's weights
   uint64_t rest;        // and of the remainder's
@@ -270,7 +284,7 @@ __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
 
 // Table entry j of factor f in [1, 2).
 __device__ __forceinline__ float2 table_entry(int j, double f) {
-  const double v = exp2((double)j / 32.0) * f;
+  const double v = kPow2[j] * f;
   const float hi = (float)v;
   return make_float2(hi, (float)(v - (double)hi));
 }
@@ -330,39 +344,37 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) acc
   if (threadIdx.x < G) {
     const int j = threadIdx.x;
     const int64_t x = a.x[(int64_t)b * G + j];
-    double ratio = 0.0;
+    float ratio = 0.f;
     if (j < nd && x >= 0 && x < a.V && s.Z[j] > 0.f) {
+      // exponents in 64 bits, the exponential in 32; below -745 a probability is zero in 64 bits too
       const int kq = G + 1 + j;
       const float tl = clean(a.target[((int64_t)b * (G + 1) + j) * a.ts + x]);
       const float dl = clean(a.draft[((int64_t)b * G + j) * a.ds + x]);
       const double zp = tl == s.M[j] ? 0.0 : ((double)tl - (double)s.M[j]) / a.temp;
       const double zq = dl == s.M[kq] ? 0.0 : ((double)dl - (double)s.M[kq]) / a.temp;
-      const bool p0 = tl == -INFINITY || exp(zp) == 0.0;
-      const bool q0 = !(s.Z[kq] > 0.f) || dl == -INFINITY || exp(zq) == 0.0;
-      if (!p0) ratio = q0 ? 1.0 : fmin(1.0, exp(zp - zq) * ((double)s.Z[kq] / (double)s.Z[j]));
+      const bool p0 = tl == -INFINITY || zp < -745.0;
+      const bool q0 = !(s.Z[kq] > 0.f) || dl == -INFINITY || zq < -745.0;
+      if (!p0) ratio = q0 ? 1.f : fminf(1.f, expf((float)(zp - zq)) * (s.Z[kq] / s.Z[j]));
     }
-    s.ratio[j] = (float)ratio;
-    if (rank == 0 && a.ratio) a.ratio[(int64_t)b * G + j] = (float)ratio;
+    s.ratio[j] = ratio;
+    if (rank == 0 && a.ratio) a.ratio[(int64_t)b * G + j] = ratio;
   }
   __syncthreads();
   if (threadIdx.x == 0) {
     int n = 0;
     while (n < nd && a.u[(int64_t)b * (G + 1) + n] < s.ratio[n]) ++n;
     s.n = n;
+    // a GPU has few fp64 lanes: the rows' scalars are formed once, not by every thread
+    s.w[0] = plain_weigh(a, s, s.M[n], s.Z[n]);
+    if (n < nd) s.w[1] = plain_weigh(a, s, s.M[G + 1 + n], s.Z[G + 1 + n]);
   }
   __syncthreads();
   const int n = s.n;
   const bool both = n < nd;
-  const Scale c = [&] {
-    const double v = 1.4426950408889634074 / a.temp;
-    const float hi = (float)v;
-    return Scale{hi, (float)(v - (double)hi)};
-  }();
+  const Scale c{a.c, a.c_lo};
   const float* pr = a.target + ((int64_t)b * (G + 1) + n) * a.ts;
   const float* qr = both ? a.draft + ((int64_t)b * G + n) * a.ds : nullptr;
-  const Weigh wp = plain_weigh(a, s, s.M[n], s.Z[n]);
-  Weigh wq{};
-  if (both) wq = plain_weigh(a, s, s.M[G + 1 + n], s.Z[G + 1 + n]);
+  const Weigh wp = s.w[0], wq = both ? s.w[1] : Weigh{};
   const bool use_q = both && !wq.none;
   // ---- this CTA's part of the vocabulary, and the sums over it
   const int64_t per = (a.V + kCluster - 1) / kCluster, i0 = min(a.V, rank * per), i1 = min(a.V, i0 + per);
@@ -392,15 +404,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) acc
     Zq += o[1];
   }
   // ---- after a rejection: the remainder max(p - q, 0)
-  Weigh np = wp, nq = wq;
   bool sub = use_q && Zp > 0;
   if (sub) {
-    double fp, fq;
-    np = normal_weigh(wp, s.table[1], Zp, &fp);
-    nq = normal_weigh(wq, s.table[2], Zq, &fq);
-    if (threadIdx.x < 64) s.table[1 + (threadIdx.x >> 5)][lane] = table_entry(lane, warp ? fq : fp);
+    if (threadIdx.x == 0) {
+      s.w[2] = normal_weigh(wp, s.table[1], Zp, &s.factor[0]);
+      s.w[3] = normal_weigh(wq, s.table[2], Zq, &s.factor[1]);
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) s.table[1 + warp][lane] = table_entry(lane, s.factor[warp]);
     __syncthreads();
   }
+  const Weigh np = sub ? s.w[2] : wp, nq = sub ? s.w[3] : wq;
   // infinite maxima: equal shares of 2^61
   const uint64_t ip = wp.inf && Zp ? (1ull << 61) / (Zp >> 30) : 0, iq = wq.inf && Zq ? (1ull << 61) / (Zq >> 30) : 0;
   auto rest = [&](int64_t i) -> uint64_t {
@@ -435,10 +449,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) acc
   }
   if (R == 0) return;
   // lowest index whose cumulative sum passes u R, in whole units
-  const float u = a.u[(int64_t)b * (G + 1) + G];
-  uint64_t goal = 0;
-  if (u >= 1.f) goal = R - 1;
-  else if (u > 0.f) goal = min(R - 1, (uint64_t)((double)u * (double)R));
+  if (threadIdx.x == 0) {
+    const float u = a.u[(int64_t)b * (G + 1) + G];
+    s.goal = u >= 1.f ? R - 1 : u > 0.f ? min(R - 1, (uint64_t)((double)u * (double)R)) : 0ull;
+  }
+  __syncthreads();
+  uint64_t goal = s.goal;
   if (goal < before || goal - before >= share) return;  // another CTA's
   goal -= before;
   for (int64_t base = i0; base < i1; base += 4 * kThreads) {
@@ -520,7 +536,11 @@ extern "C" int cas_spec_verify(const float* target, int64_t target_stride, const
   SpecArgs a{};
   a.target = target, a.draft = draft, a.u = u, a.x = x, a.n_draft = n_draft, a.ts = target_stride;
   a.ds = draft_stride, a.V = vocab, a.batch = batch, a.gamma = gamma, a.temp = temperature;
-  a.c = greedy ? 0.f : (float)(1.4426950408889634074 / temperature);
+  if (!greedy) {
+    const double c = 1.4426950408889634074 / temperature;
+    a.c = (float)c;
+    a.c_lo = (float)(c - (double)a.c);
+  }
   a.n_accepted = n_accepted, a.tokens = tokens, a.ratio = ratio, a.part = (float2*)workspace;
   const int rows = batch * (greedy ? gamma + 1 : 2 * gamma + 1);
   slice(rows, vocab, &a.slices, &a.vecs);

@@ -22,7 +22,16 @@ __device__ __forceinline__ void tm_free(uint32_t addr, uint32_t cols) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Loads complete; the registers of one load pass through, so that no use of them moves before the wait.
+__device__ __forceinline__ void tm_wait_ld(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 32 columns of the warp's 32 lanes: register j of a lane is column addr + j of
@@ -59,27 +68,47 @@ constexpr uint32_t tc_idesc_bf16(int M, int N, bool b_n_major) {
 }
 // Shared-memory operand in 128-byte swizzled atoms of 8 rows x 128 bytes (as a
 // TMA load with 128B swizzle writes them; the tile 1024-byte aligned). K-major:
-// rows are M or N, stride = bytes between atoms of 8 rows. MN-major: rows are K,
-// stride = bytes between atoms of 8 k, lead = bytes between atoms of 64 n.
-__device__ __forceinline__ uint64_t tc_desc(uint32_t smem_addr, uint32_t lead, uint32_t stride) {
-  return (uint64_t)((smem_addr & 0x3FFFF) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// rows are M or N, 1024 bytes between atoms of 8 rows. MN-major: rows are K,
+// 1024 bytes between atoms of 8 k, `lead` bytes between atoms of 64 n. The lower
+// half of a descriptor (address and lead) as a function of both; the upper half
+// (stride 1024, version 1, 128-byte swizzle) is a constant.
+constexpr uint32_t kTcDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t tc_desc_lo(uint32_t smem_addr, uint32_t lead) {
+  return ((smem_addr & 0x3FFFF) >> 4) | (lead >> 4) << 16;
 }
-// D (+)= A B, one thread issues; A in shared memory.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
 }
-// The same with A (bf16 pairs in 32-bit columns) in tensor memory.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
+// A whole product of depth 128 (eight steps of 16) in one block: the warp is
+// converged and one elected lane runs it, so that the descriptors stay in
+// uniform registers and an instruction costs few issue slots of the SM
+// sub-partition that the issuing warp shares with softmax warps (with eight
+// separate statements in one thread: 1600 instead of 1190 clocks for two
+// products while the softmax runs, 1024 by themselves).
+#define CAS_MMA_SS(P, OFF)                                                                              \
+  " add.u32 ta, %1, " #OFF ";\n add.u32 tb, %2, " #OFF ";\n mov.b64 da, {ta, %3};\n mov.b64 db, {tb, %3};\n" \
+  " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, " P ";\n"
+// D = A B^T, A [128][128] and B [128][128] bf16, both K-major in halves of 64 k that are 16 KB apart.
+__device__ __forceinline__ void tc_product_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+  asm volatile("{\n .reg .pred t, f;\n .reg .b32 ta, tb;\n .reg .b64 da, db;\n setp.eq.u32 t, 0, 0;\n"
+               " setp.ne.u32 f, 0, 0;\n" CAS_MMA_SS("f", 0) CAS_MMA_SS("t", 2) CAS_MMA_SS("t", 4) CAS_MMA_SS("t", 6)
+                   CAS_MMA_SS("t", 1024) CAS_MMA_SS("t", 1026) CAS_MMA_SS("t", 1028) CAS_MMA_SS("t", 1030) "}\n" ::"r"(d),
+               "r"(a), "r"(b), "r"(kTcDescHi), "r"(idesc)
+               : "memory");
+}
+#define CAS_MMA_TS(P, AO, BO)                                                                       \
+  " add.u32 ta, %1, " #AO ";\n add.u32 tb, %2, " #BO ";\n mov.b64 db, {tb, %3};\n"                    \
+  " tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %4, " P ";\n"
+// D (+)= A B, A [128][128] bf16 pairs in 64 columns of tensor memory, B [128 k][128] bf16 MN-major.
+__device__ __forceinline__ void tc_product_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
+  asm volatile("{\n .reg .pred t, f;\n .reg .b32 ta, tb;\n .reg .b64 db;\n setp.eq.u32 t, 0, 0;\n"
+               " setp.ne.u32 f, %5, 0;\n" CAS_MMA_TS("f", 0, 0) CAS_MMA_TS("t", 8, 128) CAS_MMA_TS("t", 16, 256)
+                   CAS_MMA_TS("t", 24, 384) CAS_MMA_TS("t", 32, 512) CAS_MMA_TS("t", 40, 640) CAS_MMA_TS("t", 48, 768)
+                       CAS_MMA_TS("t", 56, 896) "}\n" ::"r"(d),
+               "r"(a), "r"(b), "r"(kTcDescHi), "r"(idesc), "r"(add)
+               : "memory");
 }
 // The barrier completes when the tcgen05 operations that this thread issued so far have.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
@@ -93,9 +122,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 }
 // generic shared-memory writes before it are seen by the tensor cores and TMA after it
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void named_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 // 4-D tile load; coordinates innermost first, x0 * element size a multiple of 16 bytes.
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x0, int x1, int x2, int x3,
                                             uint64_t* bar) {
@@ -104,6 +130,41 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
           "r"(smem_u32(dst)),
       "l"(map), "r"(smem_u32(bar)), "r"(x0), "r"(x1), "r"(x2), "r"(x3)
       : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// ---------------------------------------------------------------- arithmetic
+// Two fp32 lanes in one instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// the largest of three; NaN loses
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
