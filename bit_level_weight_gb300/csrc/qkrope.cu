@@ -19,7 +19,9 @@
 #include <algorithm>
 #include <cmath>
 
+#include "mma.cuh"
 #include "paged.cuh"
+#include "tc05.cuh"
 
 namespace cas {
 
@@ -58,17 +60,17 @@ int check_paged(const cas_paged_kv* kv, const cas_paged_batch* b) {
 namespace {
 
 constexpr int kHeadsMax = 4096;
-constexpr int kHalfWarps = 64;  // wanted a SM before a half-warp takes more than one head
-constexpr int kHeadsPer = 12;   // heads a half-warp takes at most
-constexpr int kThreads = 256;
-constexpr int kAhead = 4;  // heads whose loads a half-warp has in flight
+constexpr int kThreads = 128;
+constexpr int kAhead = 2;         // groups of four heads whose loads a warp has in flight
+constexpr int kHeadsPer = 16;     // heads a warp takes at most: a multiple of 4
+constexpr int kWarpsWanted = 48;  // a SM, before a warp takes more than four heads
 
 struct QkArgs {
   const void* qkv;
   const uint16_t *gq, *gk;
   const int32_t* pos;
   int64_t pos0;
-  int rows, Hq, Hkv, rps, hpu;  // hpu: heads per half-warp
+  int rows, Hq, Hkv, rps, hpw, per_row;  // hpw: heads per warp, per_row: warps per row
   float eps;
   uint16_t *q, *k, *v;
   int64_t ks, vs;
@@ -76,133 +78,171 @@ struct QkArgs {
   uint64_t F[64];  // theta^(-i/64) / (2 pi) in units of 2^-64
 };
 
-__device__ __forceinline__ void unpack4(uint2 t, float x[4]) {
-  x[0] = __uint_as_float(t.x << 16), x[1] = __uint_as_float(t.x & 0xFFFF0000u);
-  x[2] = __uint_as_float(t.y << 16), x[3] = __uint_as_float(t.y & 0xFFFF0000u);
-}
+// Eight consecutive values of a head as they are loaded, and as pairs.
 template <class T>
-struct Raw;  // four values as they were loaded
+struct Raw;
 template <>
 struct Raw<float> {
-  float4 t;
-  __device__ __forceinline__ void load(const float* p) { t = *reinterpret_cast<const float4*>(p); }
-  __device__ __forceinline__ void get(float x[4]) const { x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w; }
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void get(uint64_t x[4]) const {
+    x[0] = pack2(a.x, a.y), x[1] = pack2(a.z, a.w), x[2] = pack2(b.x, b.y), x[3] = pack2(b.z, b.w);
+  }
 };
+__device__ __forceinline__ uint64_t widen2(uint32_t t) {
+  return pack2(__uint_as_float(t << 16), __uint_as_float(t & 0xFFFF0000u));
+}
 template <>
 struct Raw<uint16_t> {
-  uint2 t;
-  __device__ __forceinline__ void load(const uint16_t* p) { t = *reinterpret_cast<const uint2*>(p); }
-  __device__ __forceinline__ void get(float x[4]) const { unpack4(t, x); }
+  uint4 t;
+  __device__ __forceinline__ void load(const uint16_t* p) { t = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(uint64_t x[4]) const {
+    x[0] = widen2(t.x), x[1] = widen2(t.y), x[2] = widen2(t.z), x[3] = widen2(t.w);
+  }
 };
-__device__ __forceinline__ void store4(uint16_t* p, const float x[4]) {
-  uint2 t;
-  t.x = f2bf(x[0]) | (uint32_t)f2bf(x[1]) << 16;
-  t.y = f2bf(x[2]) | (uint32_t)f2bf(x[3]) << 16;
-  *reinterpret_cast<uint2*>(p) = t;
+__device__ __forceinline__ uint32_t round2(uint64_t v) {
+  float a, b;
+  unpack2(v, a, b);
+  return pack_bf16x2(a, b);
+}
+__device__ __forceinline__ void store8(uint16_t* p, const uint64_t x[4]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(round2(x[0]), round2(x[1]), round2(x[2]), round2(x[3]));
 }
 
-// A half-warp takes hpu consecutive heads of one row; its lane l holds the
-// values 4l..4l+3 and 64+4l..64+4l+3 of a head, so a pair stays in one lane
-// and a head's loads and stores are contiguous halves of 256 (128) bytes.
+// A warp takes hpw consecutive heads of one row, four at a time: eight lanes a
+// head, lane l of them the values 8l..8l+7 and 64+8l..64+8l+7, so that a pair
+// stays in one lane, loads and stores are 16 bytes and the arithmetic is on
+// packed pairs. The row's 64 sines and cosines: each lane forms two of the
+// eight that it needs, the quarters of the warp exchange them.
 template <class T, bool PAGED>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ QkArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 5 : 6) qk_norm_rope_kernel(const __grid_constant__ QkArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int H = a.Hq + 2 * a.Hkv;
-  const int per_row = (H + a.hpu - 1) / a.hpu;
-  const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 4;
-  const int64_t row = unit / per_row;
-  if (row >= a.rows) return;  // both halves of a warp may differ: no warp-wide operation below but within a half
-  const int h0 = (int)(unit - row * per_row) * a.hpu, h1 = min(H, h0 + a.hpu);
-  const int l = threadIdx.x & 15;
-  const uint32_t half = (threadIdx.x & 16) ? 0xFFFF0000u : 0x0000FFFFu;
-  int64_t p, page = -1, slot = 0;
-  int seq = 0;
+  const int H = a.Hq + 2 * a.Hkv, lane = threadIdx.x & 31, l = lane & 7, quarter = lane >> 3;
+  const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+  const int64_t row = unit / a.per_row;
+  if (row >= a.rows) return;
+  const int h0 = (int)(unit - row * a.per_row) * a.hpw, h1 = min(H, h0 + a.hpw);
+  const T* src = (const T*)a.qkv + (row * H + h0 + quarter) * CAS_BLK + 8 * l;
+  Raw<T> rx[kAhead], ry[kAhead];  // groups of four heads in flight
+  auto load = [&](int hb) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (hb + 4 * i + quarter < h1) {
+        const T* from = src + (int64_t)(hb + 4 * i - h0) * CAS_BLK;
+        rx[i].load(from);
+        ry[i].load(from + 64);
+      }
+  };
+  load(h0);
+  int64_t p, slot = -1;
   if (PAGED) {
     // the last sequence that starts at or before the row
-    int lo = 0, hi = a.pg.batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.pg.row_start[mid] <= row) lo = mid; else hi = mid;
+    int seq = 0;
+    if (a.pg.batch > 1) {
+      int below = 0;
+      for (int b0 = 0; b0 < a.pg.batch; b0 += 32)
+        below += __popc(__ballot_sync(CAS_FULL, b0 + lane < a.pg.batch && a.pg.row_start[b0 + lane] <= row));
+      seq = max(0, below - 1);
     }
-    seq = lo;
     const SeqSpan s = seq_span(a.pg, seq);
     if (row < s.start || row >= s.end) return;  // padding: left as it was
     p = (int64_t)s.len - (s.end - row);
-    page = page_of(a.pg, seq, p);
-    slot = page * a.pg.page_stride + (p & ((1 << a.pg.shift) - 1)) * a.pg.token_stride;
+    const int64_t page = page_of(a.pg, seq, p);
+    if (page >= 0) slot = page * a.pg.page_stride + (p & ((1 << a.pg.shift) - 1)) * a.pg.token_stride;
   } else {
     p = a.pos ? (int64_t)a.pos[row] : a.pos0 + row % a.rps;
   }
-  float cs[4], sn[4];
-  if (h0 < a.Hq + a.Hkv) {
+  uint64_t cs[4], sn[4];
+  {
+    float c[8], s[8], mc[2], ms[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int32_t turn = (int32_t)(((uint64_t)p * a.F[4 * l + j]) >> 32);
-      sincospif((float)turn * 4.656612873077392578125e-10f /* 2^-31 */, &sn[j], &cs[j]);
+    for (int j = 0; j < 2; ++j) {  // pairs 8 l + 2 quarter + j
+      const int32_t turn = (int32_t)(((uint64_t)p * a.F[8 * l + 2 * quarter + j]) >> 32);
+      sincospif((float)turn * 4.656612873077392578125e-10f /* 2^-31 */, &ms[j], &mc[j]);
     }
-  }
-  const uint2 none = make_uint2(0, 0);
-  const uint2 gq0 = a.gq ? *reinterpret_cast<const uint2*>(a.gq + 4 * l) : none;
-  const uint2 gq1 = a.gq ? *reinterpret_cast<const uint2*>(a.gq + 64 + 4 * l) : none;
-  const uint2 gk0 = a.gk ? *reinterpret_cast<const uint2*>(a.gk + 4 * l) : none;
-  const uint2 gk1 = a.gk ? *reinterpret_cast<const uint2*>(a.gk + 64 + 4 * l) : none;
-  const T* src = (const T*)a.qkv + row * H * CAS_BLK + 4 * l;
-  for (int hb = h0; hb < h1; hb += kAhead) {
-    Raw<T> rx[kAhead], ry[kAhead];  // loads of kAhead heads in flight
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (hb + i < h1) {
-        rx[i].load(src + (int64_t)(hb + i) * CAS_BLK);
-        ry[i].load(src + (int64_t)(hb + i) * CAS_BLK + 64);
-      }
+    for (int k = 0; k < 8; ++k) {
+      c[k] = __shfl_sync(CAS_FULL, mc[k & 1], (k >> 1) * 8 + l);
+      s[k] = __shfl_sync(CAS_FULL, ms[k & 1], (k >> 1) * 8 + l);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) cs[k] = pack2(c[2 * k], c[2 * k + 1]), sn[k] = pack2(s[2 * k], s[2 * k + 1]);
+  }
+  for (int hb = h0;;) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int h = hb + i;
-      if (h >= h1) break;
-      float x[4], y[4];
-      rx[i].get(x);
-      ry[i].get(y);
+      const int h = hb + 4 * i + quarter;
       const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
-      if (is_q ? a.gq != nullptr : !is_v && a.gk != nullptr) {
-        float ss = 0.f;
+      const uint16_t* g = is_q ? a.gq : is_v ? nullptr : a.gk;
+      uint64_t x[4], y[4];
+      if (h < h1) {
+        rx[i].get(x);
+        ry[i].get(y);
+      } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ss = fmaf(x[j], x[j], fmaf(y[j], y[j], ss));
+        for (int k = 0; k < 4; ++k) x[k] = y[k] = 0;
+      }
+      if (a.gq || a.gk) {  // warp-uniform: every lane takes part in the sums
+        uint64_t s2 = mul2(x[0], x[0]);
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1) ss += __shfl_xor_sync(half, ss, d);
-        const float inv = rsqrtf(ss * (1.f / CAS_BLK) + a.eps);
-        float gx[4], gy[4];
-        unpack4(is_q ? gq0 : gk0, gx);
-        unpack4(is_q ? gq1 : gk1, gy);
+        for (int k = 1; k < 4; ++k) s2 = fma2(x[k], x[k], s2);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j] *= inv * gx[j];
-          y[j] *= inv * gy[j];
+        for (int k = 0; k < 4; ++k) s2 = fma2(y[k], y[k], s2);
+        float s0, s1;
+        unpack2(s2, s0, s1);
+        float ss = s0 + s1;
+#pragma unroll
+        for (int d = 4; d > 0; d >>= 1) ss += __shfl_xor_sync(CAS_FULL, ss, d);
+        if (g) {
+          const float inv = rsqrtf(ss * (1.f / CAS_BLK) + a.eps);
+          const uint64_t i2 = pack2(inv, inv);
+          Raw<uint16_t> gr;
+          uint64_t gx[4];
+          gr.load(g + 8 * l);
+          gr.get(gx);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = mul2(mul2(x[k], i2), gx[k]);
+          gr.load(g + 64 + 8 * l);
+          gr.get(gx);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k] = mul2(mul2(y[k], i2), gx[k]);
         }
       }
       if (!is_v) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float c = x[j], d = y[j];
-          x[j] = fmaf(c, cs[j], -d * sn[j]);
-          y[j] = fmaf(d, cs[j], c * sn[j]);
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t u = x[k], w = y[k];
+          float d0, d1;
+          unpack2(mul2(w, sn[k]), d0, d1);
+          x[k] = fma2(u, cs[k], pack2(-d0, -d1));
+          y[k] = fma2(w, cs[k], mul2(u, sn[k]));
         }
       }
       uint16_t* dst;
+      bool put = h < h1;
       if (is_q) {
         dst = a.q + (row * a.Hq + h) * CAS_BLK;
       } else {
         const int hk = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
         if (PAGED) {
-          if (page < 0) continue;
+          put = put && slot >= 0;
           dst = (is_v ? a.pg.v : a.pg.k) + slot + hk * a.pg.head_stride;
         } else {
           dst = is_v ? a.v + row * a.vs + (int64_t)hk * CAS_BLK : a.k + row * a.ks + (int64_t)hk * CAS_BLK;
         }
       }
-      store4(dst + 4 * l, x);
-      store4(dst + 64 + 4 * l, y);
+      if (put) {
+        store8(dst + 8 * l, x);
+        store8(dst + 64 + 8 * l, y);
+      }
     }
+    hb += 4 * kAhead;
+    if (hb >= h1) break;
+    load(hb);
   }
 }
 
@@ -221,12 +261,15 @@ int launch_qk(QkArgs& a, int type, double theta, cudaStream_t st) {
   for (int i = 0; i < 64; ++i)  // below 2^64 / 6: the product is a whole number of 2^-64 turns
     a.F[i] = (uint64_t)std::llround(std::ldexp(std::exp(-lt * i / 64.0) / 6.283185307179586476925286766559, 62)) << 2;
   const int H = a.Hq + 2 * a.Hkv;
-  // A half-warp pays for its row's sines once, whatever number of heads it
-  // takes; few rows are spread over as many half-warps as there are heads.
-  const int64_t half_warps = (int64_t)sm_count() * kHalfWarps;
-  a.hpu = (int)std::min<int64_t>(kHeadsPer, std::max<int64_t>(1, (int64_t)a.rows * H / half_warps));
-  const int64_t units = (int64_t)a.rows * ((H + a.hpu - 1) / a.hpu);
-  const int64_t blocks = (units * 16 + kThreads - 1) / kThreads;
+  // A warp forms its row's sines once, whatever number of heads it takes; few
+  // rows are spread over more warps.
+  const int64_t warps = (int64_t)sm_count() * kWarpsWanted;
+  const int groups = (H + 3) / 4;
+  int each = (int)std::min<int64_t>(kHeadsPer / 4, std::max<int64_t>(1, (int64_t)a.rows * groups / warps));
+  a.per_row = (groups + each - 1) / each;
+  a.hpw = 4 * ((groups + a.per_row - 1) / a.per_row);
+  const int64_t units = (int64_t)a.rows * a.per_row;
+  const int64_t blocks = (units * 32 + kThreads - 1) / kThreads;
   if (blocks > 0x7FFFFFFF) return CAS_ERR_INVALID;
   return type == CAS_T_F32 ? launch_k(qk_norm_rope_kernel<float, PAGED>, (unsigned)blocks, kThreads, 0, st, a)
                            : launch_k(qk_norm_rope_kernel<uint16_t, PAGED>, (unsigned)blocks, kThreads, 0, st, a);
