@@ -7,12 +7,11 @@
 // pairs (i, i + 64) turn by p * theta^(-i/64). Each value is read once and
 // written once.
 //
-// Angle: theta^(-i/64) / 2 pi is a fraction of a turn per position, held as
-// a 64-bit fixed-point number F_i (units of 2^-64 turns). p * F_i modulo 2^64
-// is the angle reduced to a turn exactly, with an error of p * 2^-65 turns from
-// F_i's rounding, and the top 32 bits of it go to sincospif: no double
-// precision sine per row, whose 64 evaluations would cost more than the row's
-// traffic on a GPU with 2 fp64 lanes per SM and clock.
+// Angle: theta^(-i/64) / 2 pi is a fraction of a turn per position, held as a
+// 64-bit fixed-point number f_i (units of 2^-64 turns, good to 2^-53 of itself).
+// p * f_i modulo 2^64 is the angle reduced to a turn, and its top 32 bits go
+// to sincospif: no double precision sine per row, whose 64 evaluations would
+// cost more than the row's traffic on a GPU with 2 fp64 lanes a SM and clock.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -75,7 +74,7 @@ struct QkArgs {
   uint16_t *q, *k, *v;
   int64_t ks, vs;
   PagedDev pg;
-  uint64_t F[64];  // theta^(-i/64) / (2 pi) in units of 2^-64
+  uint64_t A[8], B[8];  // theta^(-i/8) / (2 pi) in units of 2^-66, theta^(-i/64) in units of 2^-63
 };
 
 // Eight consecutive values of a head as they are loaded, and as pairs.
@@ -160,8 +159,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 5 : 6) qk_norm_rope
   {
     float c[8], s[8], mc[2], ms[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {  // pairs 8 l + 2 quarter + j
-      const int32_t turn = (int32_t)(((uint64_t)p * a.F[8 * l + 2 * quarter + j]) >> 32);
+    for (int j = 0; j < 2; ++j) {  // pairs 8 l + 2 quarter + j: turns a position in units of 2^-64
+      const uint64_t f = __umul64hi(a.A[l], a.B[2 * quarter + j]) >> 1;
+      const int32_t turn = (int32_t)(((uint64_t)p * f) >> 32);
       sincospif((float)turn * 4.656612873077392578125e-10f /* 2^-31 */, &ms[j], &mc[j]);
     }
 #pragma unroll
@@ -258,8 +258,10 @@ int check_common(const void* qkv, int type, int rows, int Hq, int Hkv, const uin
 template <bool PAGED>
 int launch_qk(QkArgs& a, int type, double theta, cudaStream_t st) {
   const double lt = std::log(theta);
-  for (int i = 0; i < 64; ++i)  // below 2^64 / 6: the product is a whole number of 2^-64 turns
-    a.F[i] = (uint64_t)std::llround(std::ldexp(std::exp(-lt * i / 64.0) / 6.283185307179586476925286766559, 62)) << 2;
+  for (int i = 0; i < 8; ++i) {  // (16 constants: 64 read by 64 lanes cost a constant-cache pass each)
+    a.A[i] = (uint64_t)std::llround(std::ldexp(std::exp(-lt * i / 8.0) / 6.283185307179586476925286766559, 62)) << 4;
+    a.B[i] = (uint64_t)std::ldexp(std::exp(-lt * i / 64.0), 63);
+  }
   const int H = a.Hq + 2 * a.Hkv;
   // A warp forms its row's sines once, whatever number of heads it takes; few
   // rows are spread over more warps.

@@ -125,6 +125,15 @@ __global__ void __launch_bounds__(kStatThreads) stats_kernel(SpecArgs a) {
   const int64_t v0 = blockIdx.y * a.vecs, v1 = min(nvec, v0 + a.vecs);
   if (blockIdx.y == 0 && k == 0 && threadIdx.x == 0 && !GREEDY) a.seq[b].done = 0;
   auto load = [&](int64_t v, float x[16]) {
+    const int64_t first = v - threadIdx.x;  // of the block's 4 * kStatThreads groups
+    if (first > 0 && first + 4 * kStatThreads <= v1 && 4 * (first + 4 * kStatThreads) - mis <= a.V) {  // all whole
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 t = __ldg(base + v + i * kStatThreads);
+        x[4 * i] = t.x, x[4 * i + 1] = t.y, x[4 * i + 2] = t.z, x[4 * i + 3] = t.w;
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t g = v + i * kStatThreads;
@@ -274,8 +283,6 @@ __constant__ float2 kPow2[32] = {
     {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f},
     {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}};
 
-__device__ __forceinline__ uint64_t neg2(uint64_t v) { return v ^ 0x8000000080000000ull; }
-
 // Weights of two logits.
 __device__ __forceinline__ void weigh2(float l0, float l1, const Weigh& w, const SpecArgs& a, const float2* table,
                                        uint64_t out[2]) {
@@ -285,22 +292,23 @@ __device__ __forceinline__ void weigh2(float l0, float l1, const Weigh& w, const
     return;
   }
   auto both = [](float v) { return pack2(v, v); };
+  const uint64_t one = both(-1.f);  // negates in the multiply-add that follows
   const uint64_t ch = both(a.c);
   uint64_t x = pack2(l0, l1), e = 0;
   if (w.diff) {  // l - m as two floats
     const uint64_t l = x, m = both(w.m);
-    x = add2(l, neg2(m));
-    const uint64_t bb = add2(x, neg2(l));
-    e = mul2(add2(add2(l, neg2(add2(x, neg2(bb)))), neg2(add2(m, bb))), ch);
+    x = fma2(m, one, l);
+    const uint64_t bb = fma2(l, one, x);                                       // x - l
+    e = mul2(fma2(add2(m, bb), one, fma2(fma2(bb, one, x), one, l)), ch);      // (l - (x - bb)) - (m + bb)
   }
-  const uint64_t yh = mul2(x, ch);
-  const uint64_t yl = add2(fma2(x, both(a.c_lo), fma2(x, ch, neg2(yh))), e);
-  const uint64_t t = add2(yh, both(kMagic));  // 32 n + j in its low bits
-  const uint64_t g0 = add2(yh, neg2(add2(t, both(-kMagic))));
-  const uint64_t g = add2(g0, yl), gl = add2(yl, neg2(add2(g, neg2(g0))));
+  const uint64_t yh = mul2(x, ch), yn = mul2(yh, one);
+  const uint64_t yl = add2(fma2(x, both(a.c_lo), fma2(x, ch, yn)), e);
+  const uint64_t t = add2(yh, both(kMagic));                                   // 32 n + j in its low bits
+  const uint64_t g0 = fma2(add2(t, both(-kMagic)), one, yh);
+  const uint64_t g = add2(g0, yl), gl = fma2(fma2(g0, one, g), one, yl);
   // 2^g - 1 as h + r
-  const uint64_t h = mul2(g, both(kLn2Hi));
-  uint64_t r = fma2(g, both(kLn2Hi), neg2(h));
+  const uint64_t h = mul2(g, both(kLn2Hi)), hn = mul2(g, both(-kLn2Hi));
+  uint64_t r = fma2(g, both(kLn2Hi), hn);
   r = fma2(g, both(kLn2Lo), r);
   r = fma2(gl, both(kLn2Hi), r);
   uint64_t p = fma2(g, both(1.33335581e-3f), both(9.61812911e-3f));  // ln^5 2 / 120, ln^4 2 / 24
@@ -313,8 +321,8 @@ __device__ __forceinline__ void weigh2(float l0, float l1, const Weigh& w, const
   const float2 b0 = table[k0 & 31], b1 = table[k1 & 31];
   const uint64_t th = pack2(b0.x, b1.x), tl = pack2(b0.y, b1.y);
   const uint64_t ph = mul2(th, h), s = add2(th, ph);
-  r = fma2(th, r, fma2(th, h, neg2(ph)));
-  r = add2(r, add2(fma2(tl, h, tl), add2(ph, neg2(add2(s, neg2(th))))));
+  r = fma2(th, r, fma2(th, h, mul2(th, hn)));
+  r = add2(r, add2(fma2(tl, h, tl), fma2(fma2(th, one, s), one, ph)));
   // s: 24 bits down to 2^-24 of at most 2.1; |r| below 2^-12
   float s0, s1, r0, r1;
   unpack2(mul2(s, both(268435456.f)), s0, s1);        // 2^28
