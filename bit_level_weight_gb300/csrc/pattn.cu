@@ -56,7 +56,8 @@ constexpr uint32_t kBuf = kTile * 256;     // bytes of a K or V tile
 constexpr uint32_t kHalf = kBuf / 2;       // 64 of the 128 dimensions
 constexpr int kThreads = 384;               // three warpgroups of 168 registers a thread at launch
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;  // 2 * 216 + 72 = 3 * 168: the softmax keeps a row of S
-constexpr int kMinCells = 3;               // cells of the line a CTA takes at least
+constexpr int kUnitCells = 2;              // cells of the line for a change of units: about two tiles' time
+constexpr int kMinCells = kUnitCells + 2;  // cells a CTA takes at least
 constexpr uint32_t kSpins = 1u << 20;
 constexpr int64_t kPieceFloats = kTile + 2;  // floats a row of a partial result: output, maximum, sum
 
@@ -72,6 +73,7 @@ struct AttnArgs {
   uint32_t gmul;     // f / G = (umulhi(f, gmul) + f) >> gshift for 0 <= f < 2^31
   int gshift;
   bool wide;         // o is 32-byte aligned
+  bool q_box;        // G divides 128: Q by TMA
 };
 struct Cut {
   int pieces;        // of the unit, CTAs c .. c + pieces - 1; 0: none
@@ -107,8 +109,8 @@ __device__ __forceinline__ int unit_tiles(const Seq& s, const AttnArgs& a, int q
   const int64_t seen = min((int64_t)s.cap, (int64_t)s.len - s.T + tok + 1);
   return seen <= 0 ? 1 : (int)((seen + kTile - 1) / kTile);
 }
-// Cells of one kv head of sequence b (a lane each, warp-wide call). A unit
-// takes a cell more than its tiles: changing units costs about a tile's time.
+// Cells of one kv head of sequence b (a lane each, warp-wide call): a unit's
+// tiles behind kUnitCells for the change of units.
 __device__ int64_t head_cells(const AttnArgs& a, int b, int lane) {
   Seq s{};
   int nq = 0;
@@ -118,7 +120,7 @@ __device__ int64_t head_cells(const AttnArgs& a, int b, int lane) {
   }
   int64_t sum = 0;
   if (nq <= 4)
-    for (int i = 0; i < nq; ++i) sum += unit_tiles(s, a, i) + 1;
+    for (int i = 0; i < nq; ++i) sum += unit_tiles(s, a, i) + kUnitCells;
   unsigned big = __ballot_sync(CAS_FULL, nq > 4);
   while (big) {  // long chunks: the warp counts one together
     const int src = __ffs(big) - 1;
@@ -127,7 +129,7 @@ __device__ int64_t head_cells(const AttnArgs& a, int b, int lane) {
     const Seq t = seq_of(a, bb);
     const int n = unit_count(t);
     int part = 0;
-    for (int i = lane; i < n; i += 32) part += unit_tiles(t, a, i) + 1;
+    for (int i = lane; i < n; i += 32) part += unit_tiles(t, a, i) + kUnitCells;
     part = warp_sum(part);
     if (lane == src) sum = part;
   }
@@ -178,7 +180,7 @@ __device__ bool find_place(const AttnArgs& a, int64_t c, int grid, Line& line, P
       const Seq s = seq_of(a, p.b);
       const int nq = unit_count(s);
       for (int q0 = 0; q0 < nq; q0 += 32) {
-        const int n = q0 + lane < nq ? unit_tiles(s, a, q0 + lane) + 1 : 0;
+        const int n = q0 + lane < nq ? unit_tiles(s, a, q0 + lane) + kUnitCells : 0;
         const int up = warp_incl_add(n, lane);
         const unsigned in = __ballot_sync(CAS_FULL, up > left);
         if (in) {
@@ -248,7 +250,7 @@ __device__ __forceinline__ uint32_t k_item(int j) { return j == 0 ? 0 : 2 * j - 
 __device__ __forceinline__ uint32_t v_item(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
 
 // ---------------------------------------------------------------- units and Q
-__device__ void scheduler(const AttnArgs& a, uint8_t* q_sm, Aux* x) {
+__device__ void scheduler(const AttnArgs& a, const CUtensorMap* qm, uint8_t* q_sm, Aux* x) {
   const int lane = threadIdx.x & 31;
   Line line;
   Place p;
@@ -268,15 +270,16 @@ __device__ void scheduler(const AttnArgs& a, uint8_t* q_sm, Aux* x) {
   Seq s = seq_of(a, p.b);
   int cell = p.cell;
   uint32_t uses[2] = {0, 0};  // of the Q tiles
+  uint32_t loads = 0;         // units whose Q was fetched by TMA
   for (uint32_t u = 0;; ++u) {
     const int all = unit_tiles(s, a, p.qt);
-    const int end = (int)min((int64_t)all + 1, cell + left);
+    const int end = (int)min((int64_t)all + kUnitCells, cell + left);
     w.b = p.b, w.start = s.start, w.hk = p.hk, w.f0 = p.qt * kUnit;
     w.rows = min(kUnit, s.R - w.f0);
     w.pos0 = s.len - s.T;
     w.kv_end = min(s.cap, s.len);
-    w.t0 = max(0, cell - 1);
-    w.n = max(0, end - 1) - w.t0;
+    w.t0 = max(0, cell - kUnitCells);
+    w.n = max(0, end - kUnitCells) - w.t0;
     left -= end - cell;
     const bool two = w.rows > kTile, tile_b = !two && (u & 1);
     w.flags = (w.n == all ? kWhole : 0) | (u == 0 ? kFirst : 0) | (tile_b ? kTileB : 0);
@@ -285,44 +288,63 @@ __device__ void scheduler(const AttnArgs& a, uint8_t* q_sm, Aux* x) {
       cut.start = w.start, cut.hk = w.hk, cut.f0 = w.f0, cut.rows = w.rows;
       cut.first = u == 0 ? 0 : 1;
     }
-    // the next unit, and whether it has a tile here (its first cell is none)
-    Seq s2 = s;
-    Place p2 = p;
-    if (++p2.qt >= unit_count(s)) {
-      p2.qt = 0;
-      if (++p2.hk >= a.d.H) {
-        p2.hk = 0;
-        do s2 = ++p2.b < a.d.batch ? seq_of(a, p2.b) : Seq{};
-        while (s2.R == 0 && p2.b < a.d.batch);
-      }
-    }
-    const bool last = left < 2 || p2.b >= a.d.batch;
+    const bool last = left <= kUnitCells;  // (a next unit's first cells hold no tile)
     if (last) w.flags |= kLast;
     if (!wait(&x->u_empty[u & 1], ((u >> 1) & 1) ^ 1, x)) break;
     if (lane == 0) x->unit[u & 1] = w;
     arrive_warp(&x->u_full[u & 1]);
-    // Q: rows of 256 bytes into swizzled halves, 16 bytes a lane
+    // Q: rows of 256 bytes in swizzled halves. Rows that the unit does not have
+    // hold another sequence's or what was there: nothing of them is used.
     const int first = tile_b ? 1 : 0, count = two ? 2 : 1;
     bool ok = true;
     for (int t = first; t < first + count; ++t) ok = ok && wait(&x->q_empty[t], (uses[t]++ & 1) ^ 1, x);
     if (!ok) break;
-    const int c = lane & 15;
+    if (a.q_box) {  // boxes of the group's heads x 128 / G tokens
+      if (lane == 0) {
+        mbar_arrive_tx(&x->q_full[u & 1], count * kBuf);
+        for (int t = 0; t < count; ++t) {
+          uint8_t* dst = q_sm + (first + t) * kBuf;
+          const int tok = w.start + div_g(a, w.f0 + t * kTile);
+          tma_load_3d(dst, qm, 0, w.hk * a.G, tok, &x->q_full[u & 1]);
+          tma_load_3d(dst + kHalf, qm, 64, w.hk * a.G, tok, &x->q_full[u & 1]);
+        }
+      }
+      __syncwarp();
+      loads = u + 1;
+    } else {  // other group sizes: 16 bytes a lane
+      const int c = lane & 15, f = w.f0 + (lane >> 4);
+      int t = div_g(a, f), h = f - t * a.G;
+      const uint16_t* src = a.q + ((int64_t)(w.start + t) * a.Hq + w.hk * a.G + h) * CAS_BLK + 8 * c;
+      const int64_t next_token = (int64_t)(a.Hq - a.G) * CAS_BLK;
+      const uint32_t dst = smem_u32(q_sm) + first * kBuf + (c >> 3) * kHalf;
 #pragma unroll 4
-    for (int row = lane >> 4; row < count * kTile; row += 2) {
-      const int f = w.f0 + min(row, w.rows - 1), t = div_g(a, f), h = w.hk * a.G + (f - t * a.G);
-      const uint16_t* src = a.q + ((int64_t)(w.start + t) * a.Hq + h) * CAS_BLK + 8 * c;
-      const uint32_t dst = smem_u32(q_sm) + (first + (row >> 7)) * kBuf + (c >> 3) * kHalf + (row & 127) * 128 +
-                           (((c & 7) ^ (row & 7)) << 4);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(row < w.rows ? 16 : 0)
-                   : "memory");
+      for (int row = lane >> 4; row < w.rows; row += 2) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + (row >> 7) * kBuf + (row & 127) * 128 +
+                                                                     (((c & 7) ^ (row & 7)) << 4)),
+                     "l"(src)
+                     : "memory");
+        src += 2 * CAS_BLK;  // the group's next head but one, or that of a later token
+        for (h += 2; h >= a.G; h -= a.G) src += next_token;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_async_smem();
+      arrive_warp(&x->q_full[u & 1]);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    fence_async_smem();
-    arrive_warp(&x->q_full[u & 1]);
     if (last) break;
-    s = s2, p = p2, cell = 0;
+    cell = 0;
+    if (++p.qt >= unit_count(s)) {
+      p.qt = 0;
+      if (++p.hk >= a.d.H) {
+        p.hk = 0;
+        do s = ++p.b < a.d.batch ? seq_of(a, p.b) : Seq{};
+        while (s.R == 0 && p.b < a.d.batch);
+      }
+    }
   }
   if (lane == 0) a.cuts[blockIdx.x] = cut;
+  if (*(volatile int*)&x->abort)  // after a wait that gave up, copies in flight land before the block ends
+    for (uint32_t u = loads > 2 ? loads - 2 : 0; u < loads; ++u)
+      mbar_wait_bounded(&x->q_full[u & 1], (u >> 1) & 1, kSpins);
 }
 
 // ---------------------------------------------------------------- K and V
@@ -545,7 +567,7 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
           for (int k = 0; k < 4; ++k)
             mx[k] = max3(mx[k], __uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1]));
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * kScaleLog2;
-        const bool grow = top > m + 8.f;
+        const bool grow = mine && top > m + 8.f;
         if (done == 0) {
           m = top;
         } else if (__any_sync(CAS_FULL, grow)) {
@@ -684,7 +706,7 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
 
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap km,
-                      const __grid_constant__ CUtensorMap vm) {
+                      const __grid_constant__ CUtensorMap vm, const __grid_constant__ CUtensorMap qm) {
   extern __shared__ __align__(1024) uint8_t q_sm[];
   uint8_t* ring = q_sm + 2 * kBuf;
   Aux* x = reinterpret_cast<Aux*>(ring + kRing * kBuf);
@@ -716,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 8) tma_prefetch_map(&km);
   if (warp == 10) tma_prefetch_map(&vm);
+  if (warp == 11 && a.q_box) tma_prefetch_map(&qm);
   if (warp == 9) tm_alloc(&x->tmem, 512);
   tc_fence_before();
   __syncthreads();
@@ -734,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (warp == 9)
       issuer(smem_u32(q_sm), smem_u32(ring), x);
     else
-      scheduler(a, q_sm, x);
+      scheduler(a, &qm, q_sm, x);
   }
   __syncwarp();
   tc_fence_before();
@@ -747,11 +770,11 @@ static_assert(kSmem <= 232448, "shared memory of a CTA");
 
 // ---------------------------------------------------------------- joining the pieces
 // Block (c, y) merges a part of the pieces of the unit whose first cut lies
-// behind CTA c: 16 of the 128 values of its rows. An item is 4 values of a row,
+// behind CTA c: 128 / gridDim.y of the values of its rows. An item is 4 values of a row,
 // neighbouring threads take neighbouring rows; where there are fewer items than
 // threads, several threads share an item's pieces, so that all loads are in
 // flight together.
-constexpr int kJoinThreads = 256, kJoinSplit = 8;
+constexpr int kJoinThreads = 256;
 struct Part {
   float m, l;
   float4 o;
@@ -772,14 +795,14 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
   pdl_trigger();
   const Cut cut = a.cuts[blockIdx.x];
   if (cut.pieces < 2) return;
-  const int items = cut.rows * (32 / kJoinSplit);
+  const int chunks = 32 / gridDim.y, items = cut.rows * chunks;
   int width = 4;  // threads side by side on items: a power of two
   while (width < items && width < kJoinThreads) width *= 2;
   const int share = kJoinThreads / width, mine = threadIdx.x & (width - 1), sub = threadIdx.x / width;
   const int64_t size = (int64_t)a.piece_rows * kPieceFloats, half = (int64_t)CAS_BLK * a.piece_rows;
   const float* base = a.ws + (int64_t)2 * blockIdx.x * size;
   for (int i0 = 0; i0 < items; i0 += width) {
-    const int i = i0 + mine, q = i / cut.rows, fr = i - q * cut.rows, c = blockIdx.y * (32 / kJoinSplit) + q;
+    const int i = i0 + mine, q = i / cut.rows, fr = i - q * cut.rows, c = blockIdx.y * chunks + q;
     Part p{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     if (i < items) {
 #pragma unroll 4
@@ -840,6 +863,19 @@ bool make_map(CUtensorMap* m, const cas_paged_kv* kv, uint16_t* pool) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// (d, head, token) of q, boxes of 64 dimensions x G heads x 128 / G tokens: 128 flat rows.
+bool make_q_map(CUtensorMap* m, const uint16_t* q, int rows, int Hq, int G) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {CAS_BLK, (cuuint64_t)Hq, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {CAS_BLK * 2, (cuuint64_t)Hq * CAS_BLK * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(kTile / G)};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(q), dims, strides, box, elem,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int piece_rows(int rows, int Hq, int Hkv) {
   const int64_t flat = (int64_t)std::max(rows, 1) * (Hq / std::max(Hkv, 1));
   return (int)std::min<int64_t>(kUnit, (flat + 31) / 32 * 32);
@@ -890,12 +926,15 @@ extern "C" int cas_paged_attn(const cas_paged_kv* kv, const cas_paged_batch* b, 
   a.piece_rows = piece_rows(b->rows, n_q_heads, kv->n_kv_heads);
   while ((1 << a.gshift) < a.G) ++a.gshift;
   a.gmul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << a.gshift) - a.G)) / a.G + 1);
-  CUtensorMap km, vm;
-  if (!make_map(&km, kv, kv->k) || !make_map(&vm, kv, kv->v)) return CAS_ERR_CUDA;
+  a.q_box = kTile % a.G == 0;
+  CUtensorMap km, vm, qm{};
+  if (!make_map(&km, kv, kv->k) || !make_map(&vm, kv, kv->v) || (a.q_box && !make_q_map(&qm, q, b->rows, n_q_heads, a.G)))
+    return CAS_ERR_CUDA;
   if (occupancy((const void*)paged_attn_kernel, kThreads, kSmem) < 1) return CAS_ERR_CUDA;
   const cudaStream_t st = (cudaStream_t)stream;
-  if (const int e = launch_k(paged_attn_kernel, grid, kThreads, kSmem, st, a, km, vm)) return e;
+  if (const int e = launch_k(paged_attn_kernel, grid, kThreads, kSmem, st, a, km, vm, qm)) return e;
   if (grid < 2) return CAS_OK;
   // directly behind our own kernel: its launch may overlap that kernel's tail
-  return launch_with(true, attn_join_kernel, dim3(grid - 1, kJoinSplit), kJoinThreads, 0, st, a);
+  // (pieces of 256 rows: two items a thread; of few rows: all in flight together)
+  return launch_with(true, attn_join_kernel, dim3(grid - 1, a.piece_rows > 128 ? 16 : 8), kJoinThreads, 0, st, a);
 }
