@@ -19,15 +19,15 @@
 // and odd ones in slot 1 and merge the two at the end, so that one slot's
 // softmax runs while the tensor cores work for the other in both cases.
 //
-//   warps 0-3, 4-7  softmax of slot 0, 1: S from tensor memory (a row a
+//   warps 4-7, 8-11 softmax of slot 0, 1: S from tensor memory (a row a
 //                   thread), P back as bf16, O rescaled there when a row's
 //                   maximum grows by more than 2^8 (probabilities relative to
 //                   an older maximum are as exact), epilogue
-//   warp 8, 10      TMA: K and V tiles from their pages, five 32 KB buffers
-//   warp 9          issues tcgen05.mma: S = Q K^T (both from shared memory),
+//   warp 1, 2       TMA: K and V tiles from their pages, five 32 KB buffers
+//   warp 0          issues tcgen05.mma: S = Q K^T (both from shared memory),
 //                   O += P V (P from tensor memory, V with the head dimension
 //                   contiguous)
-//   warp 11         finds the CTA's units and hands them to the others one
+//   warp 3          finds the CTA's units and hands them to the others one
 //                   ahead, with their Q rows
 //
 // Every wait is bounded: one that gives up marks the CTA, whose warps then
@@ -511,7 +511,7 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v, bool wide) {
 }
 
 __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
-  const int slot = threadIdx.x >> 7, r = threadIdx.x & 127, warp = r >> 5;
+  const int slot = (threadIdx.x >> 7) - 1, r = threadIdx.x & 127, warp = r >> 5;
   const uint32_t tm = x->tmem + ((uint32_t)warp << 21);
   const uint32_t tm_s = tm + slot * kTile, tm_o = tm + 2 * kTile + slot * CAS_BLK;
   uint32_t base = 0, ns = 0, no = 0, nm = 0;
@@ -736,25 +736,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     fence_async_smem();
   }
-  if (warp == 8) tma_prefetch_map(&km);
-  if (warp == 10) tma_prefetch_map(&vm);
-  if (warp == 11 && a.q_box) tma_prefetch_map(&qm);
-  if (warp == 9) tm_alloc(&x->tmem, 512);
+  if (warp == 1) tma_prefetch_map(&km);
+  if (warp == 2) tma_prefetch_map(&vm);
+  if (warp == 3 && a.q_box) tma_prefetch_map(&qm);
+  if (warp == 0) tm_alloc(&x->tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   pdl_wait();
   pdl_trigger();
-  if (warp < 8) {
+  if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     softmax(a, ring, x);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == 8)
+    if (warp == 1)
       producer<false>(a, &km, ring, x);
-    else if (warp == 10)
+    else if (warp == 2)
       producer<true>(a, &vm, ring, x);
-    else if (warp == 9)
+    else if (warp == 0)
       issuer(smem_u32(q_sm), smem_u32(ring), x);
     else
       scheduler(a, &qm, q_sm, x);
@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tm_free(x->tmem, 512);
+  if (warp == 0) tm_free(x->tmem, 512);
 }
 constexpr size_t kSmem = (2 + kRing) * (size_t)kBuf + sizeof(Aux);
 static_assert(kSmem <= 232448, "shared memory of a CTA");
