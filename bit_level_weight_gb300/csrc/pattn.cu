@@ -245,9 +245,18 @@ __device__ __forceinline__ bool take_unit(uint32_t u, Aux* x, Unit& w) {
   return true;
 }
 
-// Ring position of K and V tile j of n: K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
-__device__ __forceinline__ uint32_t k_item(int j) { return j == 0 ? 0 : 2 * j - 1; }
-__device__ __forceinline__ uint32_t v_item(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
+// K and V tiles take the buffers in turn: K0 V0 K1 V1 ... A turn is a buffer and
+// the parity of its use; each of the two streams takes every second one.
+struct Turn {
+  uint32_t slot, phase;
+  __device__ __forceinline__ void next() {
+    slot += 2;
+    if (slot >= kRing) {
+      slot -= kRing;
+      phase ^= 1;
+    }
+  }
+};
 
 // ---------------------------------------------------------------- units and Q
 __device__ void scheduler(const AttnArgs& a, const CUtensorMap* qm, uint8_t* q_sm, Aux* x) {
@@ -355,7 +364,7 @@ __device__ void producer(const AttnArgs& a, const CUtensorMap* map, uint8_t* rin
   const int lane = threadIdx.x & 31;
   const int shift = min(a.d.shift, 7);  // log2 of tokens a box
   const int boxes = kTile >> shift;     // boxes a tile
-  uint32_t base = 0;
+  Turn turn{IS_V ? 1u : 0u, 0};
   uint32_t used = 0, phase = 0;  // buffers this warp has filled, and the phase of its newest copy
   bool ok = true;
   for (uint32_t u = 0; ok; ++u) {
@@ -370,11 +379,12 @@ __device__ void producer(const AttnArgs& a, const CUtensorMap* map, uint8_t* rin
     };
     int cur = page_at(0), nxt = page_at(1);
     for (int j = 0; j < w.n; ++j) {
-      const uint32_t it = base + (IS_V ? v_item(j, w.n) : k_item(j)), slot = it % kRing;
-      ok = wait(&x->kv_empty[slot], ((it / kRing) & 1) ^ 1, x);
+      const uint32_t slot = turn.slot;
+      ok = wait(&x->kv_empty[slot], turn.phase ^ 1, x);
       if (!ok) break;
       used |= 1u << slot;
-      phase = (phase & ~(1u << slot)) | ((it / kRing) & 1) << slot;
+      phase = (phase & ~(1u << slot)) | turn.phase << slot;
+      turn.next();
       if (lane == 0) mbar_arrive_tx(&x->kv_full[slot], kBuf);
       __syncwarp();
       if (lane < boxes) {
@@ -386,7 +396,6 @@ __device__ void producer(const AttnArgs& a, const CUtensorMap* map, uint8_t* rin
       cur = nxt;
       nxt = page_at(j + 2);
     }
-    base += 2 * w.n;
     if (w.flags & kLast) break;
   }
   // after a wait that gave up, copies in flight land before the block ends
@@ -396,98 +405,114 @@ __device__ void producer(const AttnArgs& a, const CUtensorMap* map, uint8_t* rin
 }
 
 // ---------------------------------------------------------------- products
+// A step of a slot is P V of one tile and the scores of the next: one elected
+// lane issues both and their signals without a wait in between, since the K and
+// V tiles that it needs are waited for before P is (they are there long since).
 __device__ void issuer(uint32_t q_sm, uint32_t ring_sm, Aux* x) {
   const uint32_t tm = __reduce_max_sync(CAS_FULL, x->tmem);
   constexpr uint32_t id_s = tc_idesc_bf16(kTile, kTile, false), id_o = tc_idesc_bf16(kTile, CAS_BLK, true);
-  uint32_t base = 0, np[2] = {0, 0};
+  uint32_t np[2] = {0, 0};
+  Turn kt{0, 0}, vt{1, 0};  // buffers of the next K and V tile
   bool ok = true;
-  auto wait_kv = [&](uint32_t item) {
-    const uint32_t it = base + item;
-    ok = ok && wait(&x->kv_full[it % kRing], (it / kRing) & 1, x);
-  };
-  auto free_kv = [&](uint32_t item) {
-    if (ok && elect_one()) tc_commit(&x->kv_empty[(base + item) % kRing]);
-  };
-  auto signal = [&](uint64_t* bar) {
-    if (ok && elect_one()) tc_commit(bar);
-  };
-  auto mma_s = [&](int slot, uint32_t tile, uint32_t item) {
-    const uint32_t buf = __shfl_sync(CAS_FULL, (base + item) % kRing, 0);
+  auto arrived = [&](const Turn& t) { ok = ok && wait(&x->kv_full[t.slot], t.phase, x); };
+  auto wait_p = [&](int slot) {
+    ok = ok && wait(&x->p_full[slot], np[slot]++ & 1, x);
     tc_fence_after();
-    if (ok && elect_one()) {
-      tc_product_ss(tm + slot * kTile, tc_desc_lo(q_sm + tile * kBuf, 16), tc_desc_lo(ring_sm + buf * kBuf, 16), id_s);
-      tc_commit(&x->s_full[slot]);
-    }
   };
-  auto mma_o = [&](int slot, uint32_t item, bool add) {
-    const uint32_t buf = __shfl_sync(CAS_FULL, (base + item) % kRing, 0);
-    tc_fence_after();
-    if (ok && elect_one())
-      tc_product_ts(tm + 2 * kTile + slot * CAS_BLK, tm + slot * kTile, tc_desc_lo(ring_sm + buf * kBuf, kHalf), id_o,
-                    add);
+  auto scores = [&](int slot, uint32_t tile, const Turn& k) {
+    tc_product_ss(tm + slot * kTile, tc_desc_lo(q_sm + tile * kBuf, 16), tc_desc_lo(ring_sm + k.slot * kBuf, 16), id_s);
+    tc_commit(&x->s_full[slot]);
   };
-  auto wait_p = [&](int slot) { ok = ok && wait(&x->p_full[slot], np[slot]++ & 1, x); };
+  auto values = [&](int slot, const Turn& v, bool add) {
+    tc_product_ts(tm + 2 * kTile + slot * CAS_BLK, tm + slot * kTile, tc_desc_lo(ring_sm + v.slot * kBuf, kHalf), id_o,
+                  add);
+  };
+  auto release = [&](const Turn& t) { tc_commit(&x->kv_empty[t.slot]); };
   for (uint32_t u = 0; ok; ++u) {
     Unit w;
     if (!take_unit(u, x, w) || (w.flags & kNone)) break;
     ok = wait(&x->q_full[u & 1], (u >> 1) & 1, x);
     const int n = w.n;
     if (w.rows > kTile) {
-      wait_kv(k_item(0));
-      mma_s(0, 0, k_item(0));
-      mma_s(1, 1, k_item(0));
-      free_kv(k_item(0));
-      if (n == 1) signal(&x->q_empty[0]), signal(&x->q_empty[1]);
+      arrived(kt);
+      tc_fence_after();
+      if (ok && elect_one()) {
+        scores(0, 0, kt);
+        scores(1, 1, kt);
+        release(kt);
+        if (n == 1) tc_commit(&x->q_empty[0]), tc_commit(&x->q_empty[1]);
+      }
+      __syncwarp();
+      kt.next();
       for (int j = 0; j < n && ok; ++j) {
-        const uint32_t v = v_item(j, n), k = k_item(j + 1);
-        const bool more = j + 1 < n;
+        const bool more = j + 1 < n, last = j + 2 == n;
+        arrived(vt);
+        if (more) arrived(kt);
         wait_p(0);
-        wait_kv(v);
-        mma_o(0, v, j > 0);
-        if (more) {
-          wait_kv(k);
-          mma_s(0, 0, k);
-          if (j + 2 == n) signal(&x->q_empty[0]);
-        } else {
-          signal(&x->o_full[0]);
+        if (ok && elect_one()) {
+          values(0, vt, j > 0);
+          if (more) {
+            scores(0, 0, kt);
+            if (last) tc_commit(&x->q_empty[0]);
+          } else {
+            tc_commit(&x->o_full[0]);
+          }
         }
+        __syncwarp();
         wait_p(1);
-        mma_o(1, v, j > 0);
-        free_kv(v);
-        if (more) {
-          mma_s(1, 1, k);
-          free_kv(k);
-          if (j + 2 == n) signal(&x->q_empty[1]);
-        } else {
-          signal(&x->o_full[1]);
+        if (ok && elect_one()) {
+          values(1, vt, j > 0);
+          release(vt);
+          if (more) {
+            scores(1, 1, kt);
+            release(kt);
+            if (last) tc_commit(&x->q_empty[1]);
+          } else {
+            tc_commit(&x->o_full[1]);
+          }
         }
+        __syncwarp();
+        vt.next();
+        if (more) kt.next();
       }
     } else {
       const int t = (w.flags & kTileB) ? 1 : 0;
       for (int j = 0; j < min(n, 2); ++j) {
-        wait_kv(k_item(j));
-        mma_s(j, t, k_item(j));
-        free_kv(k_item(j));
-        if (j + 1 == n) signal(&x->q_empty[t]);
+        arrived(kt);
+        tc_fence_after();
+        if (ok && elect_one()) {
+          scores(j, t, kt);
+          release(kt);
+          if (j + 1 == n) tc_commit(&x->q_empty[t]);
+        }
+        __syncwarp();
+        kt.next();
       }
       for (int j = 0; j < n && ok; ++j) {
         const int i = j & 1;
-        const uint32_t v = v_item(j, n), k = k_item(j + 2);
+        const bool more = j + 2 < n;
+        // few rows wait for memory: nothing waits for a K tile that it does not need
+        arrived(vt);
         wait_p(i);
-        wait_kv(v);
-        mma_o(i, v, j >= 2);
-        free_kv(v);
-        if (j + 2 < n) {
-          wait_kv(k);
-          mma_s(i, t, k);
-          free_kv(k);
-          if (j + 3 == n) signal(&x->q_empty[t]);
-        } else {
-          signal(&x->o_full[i]);
+        if (ok && elect_one()) {
+          values(i, vt, j >= 2);
+          release(vt);
+          if (!more) tc_commit(&x->o_full[i]);
         }
+        __syncwarp();
+        if (more) {
+          arrived(kt);
+          if (ok && elect_one()) {
+            scores(i, t, kt);
+            release(kt);
+            if (j + 3 == n) tc_commit(&x->q_empty[t]);
+          }
+          __syncwarp();
+        }
+        vt.next();
+        if (more) kt.next();
       }
     }
-    base += 2 * n;
     if (w.flags & kLast) break;
   }
   if (elect_one()) tc_commit(&x->drain);  // products in flight end before the block does
@@ -514,7 +539,7 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
   const int slot = (threadIdx.x >> 7) - 1, r = threadIdx.x & 127, warp = r >> 5;
   const uint32_t tm = x->tmem + ((uint32_t)warp << 21);
   const uint32_t tm_s = tm + slot * kTile, tm_o = tm + 2 * kTile + slot * CAS_BLK;
-  uint32_t base = 0, ns = 0, no = 0, nm = 0;
+  uint32_t base = 0, ns = 0, no = 0, nm = 0;  // base: tiles of the units before
   bool pending = false;  // the other slot may still read this slot's O
   for (uint32_t u = 0;; ++u) {
     Unit w;
@@ -611,7 +636,7 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
       ++done;
       if (key0 + kTile > w.kv_end && (slot == 0 || !two)) {
         // slots behind the last token may hold anything: their V rows become zeros
-        const uint32_t it = base + v_item(j, w.n);
+        const uint32_t it = 2 * (base + j) + 1;
         if (!wait(&x->kv_full[it % kRing], (it / kRing) & 1, x)) return;
         if (key0 + r >= w.kv_end) {
           uint4* row = reinterpret_cast<uint4*>(ring + (it % kRing) * kBuf + r * 128);
@@ -627,7 +652,7 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
       }
       arrive_warp(&x->p_full[slot]);
     }
-    base += 2 * w.n;
+    base += w.n;
     // ---- epilogue
     if (pending) {  // (no tile was this slot's)
       if (!wait(&x->merged, (nm - 1) & 1, x)) return;
