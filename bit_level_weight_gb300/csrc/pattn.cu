@@ -109,9 +109,9 @@ __device__ __forceinline__ int unit_tiles(const Seq& s, const AttnArgs& a, int q
   const int64_t seen = min((int64_t)s.cap, (int64_t)s.len - s.T + tok + 1);
   return seen <= 0 ? 1 : (int)((seen + kTile - 1) / kTile);
 }
-// Cells of one kv head of sequence b (a lane each, warp-wide call): a unit's
-// tiles behind kUnitCells for the change of units.
-__device__ int64_t head_cells(const AttnArgs& a, int b, int lane) {
+// Cells of one kv head of sequence b (a lane each, warp-wide call; b beyond the
+// batch: none): a unit's tiles behind kUnitCells for the change of units.
+__device__ __forceinline__ int64_t head_cells(const AttnArgs& a, int b, int lane) {
   Seq s{};
   int nq = 0;
   if (b < a.d.batch) {
@@ -135,6 +135,14 @@ __device__ int64_t head_cells(const AttnArgs& a, int b, int lane) {
   }
   return sum;
 }
+__device__ __forceinline__ int64_t warp_incl64(int64_t v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t u = __shfl_up_sync(CAS_FULL, v, d);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
 
 struct Place {
   int b, hk, qt, cell;  // unit and the cell inside it
@@ -144,64 +152,65 @@ struct Line {
 };
 
 // Warp-wide: the line's length, and the place of cell `c * per` on it (false
-// when the line is shorter).
+// when the line is shorter). A lane adds up `each` neighbouring sequences; the
+// lane that holds the place has its sequences looked at again by the warp.
 __device__ bool find_place(const AttnArgs& a, int64_t c, int grid, Line& line, Place& p) {
   const int lane = threadIdx.x & 31;
-  int64_t total = 0, first = 0;
-  for (int b0 = 0; b0 < a.d.batch; b0 += 32) {
-    int64_t t = head_cells(a, b0 + lane, lane);
-    if (b0 == 0) first = t;
-    t *= a.d.H;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(CAS_FULL, t, d);
-    total += t;
-  }
-  line.total = total;
-  line.per = max((int64_t)kMinCells, div64(total + grid - 1, grid));
+  const int each = (a.d.batch + 31) / 32;
+  int64_t own = 0;
+#pragma unroll 1
+  for (int k = 0; k < each; ++k) own += head_cells(a, lane * each + k, lane);
+  int64_t incl = warp_incl64(own, lane);
+  line.total = __shfl_sync(CAS_FULL, incl, 31) * a.d.H;
+  line.per = max((int64_t)kMinCells, div64(line.total + grid - 1, grid));
   const int64_t want = c * line.per;
-  if (want >= total) return false;
-  int64_t base = 0;
-  for (int b0 = 0; b0 < a.d.batch; b0 += 32) {
-    const int64_t h = b0 == 0 ? first : head_cells(a, b0 + lane, lane), t = h * a.d.H;
-    int64_t incl = t;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t u = __shfl_up_sync(CAS_FULL, incl, d);
-      if (lane >= d) incl += u;
-    }
-    const unsigned hit = __ballot_sync(CAS_FULL, base + incl > want);
+  if (want >= line.total) return false;
+  // the sequence whose cells, of all its heads, hold the wanted one
+  unsigned hit = __ballot_sync(CAS_FULL, incl * a.d.H > want);
+  int src = __ffs(hit) - 1;
+  int64_t before = __shfl_sync(CAS_FULL, incl - own, src), per_head = __shfl_sync(CAS_FULL, own, src);
+  p.b = src * each;
+#pragma unroll 1
+  for (int k0 = 0; each > 1 && k0 < each; k0 += 32) {
+    const int b = src * each + k0 + lane;
+    const int64_t h = head_cells(a, k0 + lane < each ? b : a.d.batch, lane);
+    incl = warp_incl64(h, lane);
+    hit = __ballot_sync(CAS_FULL, (before + incl) * a.d.H > want);
     if (hit) {
-      const int src = __ffs(hit) - 1;
-      const int64_t before = base + __shfl_sync(CAS_FULL, incl - t, src);
-      const int64_t per_head = __shfl_sync(CAS_FULL, h, src);
-      p.b = b0 + src;
-      p.hk = (int)div64(want - before, per_head);
-      int64_t left = want - before - p.hk * per_head;
-      const Seq s = seq_of(a, p.b);
-      const int nq = unit_count(s);
-      for (int q0 = 0; q0 < nq; q0 += 32) {
-        const int n = q0 + lane < nq ? unit_tiles(s, a, q0 + lane) + kUnitCells : 0;
-        const int up = warp_incl_add(n, lane);
-        const unsigned in = __ballot_sync(CAS_FULL, up > left);
-        if (in) {
-          const int w = __ffs(in) - 1;
-          p.qt = q0 + w;
-          p.cell = (int)(left - __shfl_sync(CAS_FULL, up - n, w));
-          return true;
-        }
-        left -= __shfl_sync(CAS_FULL, up, 31);
-      }
-      return false;  // not reached: the unit lies in the sequence
+      const int w = __ffs(hit) - 1;
+      p.b += k0 + w;
+      per_head = __shfl_sync(CAS_FULL, h, w);
+      before += __shfl_sync(CAS_FULL, incl - h, w);
+      break;
     }
-    base += __shfl_sync(CAS_FULL, incl, 31);
+    before += __shfl_sync(CAS_FULL, incl, 31);
   }
-  return false;
+  int64_t left = want - before * a.d.H;
+  if (!hit || per_head <= 0) return false;  // not reached: the sequence lies in the lane's
+  p.hk = (int)div64(left, per_head);
+  left -= p.hk * per_head;
+  const Seq s = seq_of(a, p.b);
+  const int nq = unit_count(s);
+  for (int q0 = 0; q0 < nq; q0 += 32) {
+    const int n = q0 + lane < nq ? unit_tiles(s, a, q0 + lane) + kUnitCells : 0;
+    const int up = warp_incl_add(n, lane);
+    const unsigned in = __ballot_sync(CAS_FULL, up > left);
+    if (in) {
+      const int w = __ffs(in) - 1;
+      p.qt = q0 + w;
+      p.cell = (int)(left - __shfl_sync(CAS_FULL, up - n, w));
+      return true;
+    }
+    left -= __shfl_sync(CAS_FULL, up, 31);
+  }
+  return false;  // not reached: the unit lies in the sequence
 }
 
 // A unit, or the part of it that a CTA takes.
 struct Unit {
   int b, start, hk, f0, rows;  // sequence and its first row, kv head, flat rows
   int pos0, kv_end;            // position of the sequence's first row, end of what it holds
+  int first_pos;               // position of the unit's first row
   int t0, n;                   // key tiles
   int flags;                   // below
 };
@@ -211,10 +220,15 @@ enum { kWhole = 1, kFirst = 2, kLast = 4, kNone = 8, kTileB = 16 };  // kTileB: 
 struct Aux {
   uint64_t kv_full[kRing], kv_empty[kRing];
   uint64_t u_full[2], u_empty[2], q_full[2], q_empty[2];
-  uint64_t s_full[2], p_full[2], o_full[2], merge, merged, drain;
+  uint64_t s_full[2], p_full[2], o_full[2], merge, merged, spoilt, drain;
   uint32_t tmem;
   int abort;
   Unit unit[2];
+  // values that are not finite and that not every row of the unit sees, for the
+  // unit at hand and the next (one slot may be ahead): whether there are any, and
+  // the first position for each dimension, counted from the unit's first row's
+  int any_bad[2];
+  uint16_t bad[2][CAS_BLK];
   float m[2][kTile], l[2][kTile];
 };
 
@@ -287,6 +301,7 @@ __device__ void scheduler(const AttnArgs& a, const CUtensorMap* qm, uint8_t* q_s
     w.rows = min(kUnit, s.R - w.f0);
     w.pos0 = s.len - s.T;
     w.kv_end = min(s.cap, s.len);
+    w.first_pos = w.pos0 + div_g(a, w.f0);
     w.t0 = max(0, cell - kUnitCells);
     w.n = max(0, end - kUnitCells) - w.t0;
     left -= end - cell;
@@ -535,15 +550,63 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v, bool wide) {
   }
 }
 
+// A probability of zero does not hide what is not finite: 0 * NaN would reach
+// rows that do not see the token. Tiles at the end of what a unit's rows see are
+// looked over by a thread a V row: rows behind the last token, which may hold
+// anything, become zeros; values of tokens that only some rows see become zeros
+// where they are not finite, and the epilogue makes the outputs of that
+// dimension NaN for the rows that see the first of them.
+__device__ __forceinline__ bool guards(const Unit& w, int key0) {
+  return min(key0 + kTile, w.kv_end) - 1 > w.first_pos;  // a token that the unit's first row does not see
+}
+__device__ bool guard_values(const Unit& w, int turn, int key0, uint32_t item, uint8_t* ring, Aux* x) {
+  const int r = threadIdx.x & 127;
+  if (!wait(&x->kv_full[item % kRing], (item / kRing) & 1, x)) return false;
+  uint8_t* row = ring + (item % kRing) * kBuf + r * 128;
+  if (key0 + r >= w.kv_end) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      *reinterpret_cast<uint4*>(row + c * 16) = *reinterpret_cast<uint4*>(row + kHalf + c * 16) = make_uint4(0, 0, 0, 0);
+  } else if (key0 + r > w.first_pos) {
+    uint32_t top = 0;  // the largest magnitudes of two lanes
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {  // rotated, so that a warp's threads read different banks
+        const uint4 v = *reinterpret_cast<const uint4*>(row + h * kHalf + (((c + r) & 7) << 4));
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                     __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+      }
+    }
+    if ((top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u) {
+      for (int d = 0; d < CAS_BLK; ++d) {
+        uint16_t* p = reinterpret_cast<uint16_t*>(row + (d >> 6) * kHalf + ((((d >> 3) & 7) ^ (r & 7)) << 4)) + (d & 7);
+        if ((*p & 0x7F80u) == 0x7F80u) {
+          *p = 0;
+          const uint16_t at = (uint16_t)(key0 + r - w.first_pos);
+          for (uint16_t old = x->bad[turn][d]; at < old;) {
+            const uint16_t was = atomicCAS(&x->bad[turn][d], old, at);
+            if (was == old) break;
+            old = was;
+          }
+          x->any_bad[turn] = 1;
+        }
+      }
+    }
+  }
+  fence_async_smem();
+  return true;
+}
+
 __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
   const int slot = (threadIdx.x >> 7) - 1, r = threadIdx.x & 127, warp = r >> 5;
   const uint32_t tm = x->tmem + ((uint32_t)warp << 21);
   const uint32_t tm_s = tm + slot * kTile, tm_o = tm + 2 * kTile + slot * CAS_BLK;
-  uint32_t base = 0, ns = 0, no = 0, nm = 0;  // base: tiles of the units before
+  uint32_t base = 0, ns = 0, no = 0, nm = 0, nb = 0;  // base: tiles of the units before
   bool pending = false;  // the other slot may still read this slot's O
+  Unit w;
+  if (!take_unit(0, x, w) || (w.flags & kNone)) return;
   for (uint32_t u = 0;; ++u) {
-    Unit w;
-    if (!take_unit(u, x, w) || (w.flags & kNone)) return;
     const bool two = w.rows > kTile;  // both slots share the key tiles
     // this thread's row: the last position it sees (-1: none)
     const int fr = two ? slot * kTile + r : r;
@@ -634,16 +697,8 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
         tm_wait_st();
       }
       ++done;
-      if (key0 + kTile > w.kv_end && (slot == 0 || !two)) {
-        // slots behind the last token may hold anything: their V rows become zeros
-        const uint32_t it = 2 * (base + j) + 1;
-        if (!wait(&x->kv_full[it % kRing], (it / kRing) & 1, x)) return;
-        if (key0 + r >= w.kv_end) {
-          uint4* row = reinterpret_cast<uint4*>(ring + (it % kRing) * kBuf + r * 128);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) row[c] = row[kHalf / 16 + c] = make_uint4(0, 0, 0, 0);
-        }
-        fence_async_smem();
+      if ((slot == 0 || !two) && (key0 + kTile > w.kv_end || guards(w, key0))) {
+        if (!guard_values(w, u & 1, key0, 2 * (base + j) + 1, ring, x)) return;
       }
       tc_fence_before();
       if (pending) {
@@ -681,6 +736,7 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
       c0 = 2 * slot;
       c1 = c0 + 2;
     }
+    const bool spoilt = *(volatile int*)&x->any_bad[u & 1];  // (the tiles' products follow the look at their values)
     if (busy) {
       const bool whole = w.flags & kWhole;
       const float inv = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
@@ -718,14 +774,33 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
           }
         }
       }
+      if (spoilt && mine) {
+#pragma unroll 1
+        for (int d = 32 * c0; d < 32 * c1; ++d)
+          if (lim - w.first_pos >= (int)x->bad[u & 1][d]) {
+            if (whole)
+              out[d] = 0x7FC0;
+            else
+              part[((int64_t)(d >> 2) * a.piece_rows + fr) * 4 + (d & 3)] = __uint_as_float(0x7FC00000u);
+          }
+      }
     }
     tc_fence_before();
+    if (spoilt) {  // clean for the next unit, when all have read it
+      arrive_warp(&x->spoilt);
+      if (!wait(&x->spoilt, nb++ & 1, x)) return;
+      if (slot == 0) x->bad[u & 1][r] = 0xFFFF;
+      x->any_bad[u & 1] = 0;
+      arrive_warp(&x->spoilt);
+      if (!wait(&x->spoilt, nb++ & 1, x)) return;
+    }
     if (!two) {  // both slots' O, m and l are read before either is written again
       arrive_warp(&x->merged);
       ++nm;
       pending = true;
     }
     if (w.flags & kLast) return;
+    if (!take_unit(u + 1, x, w)) return;
   }
 }
 
@@ -756,14 +831,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&x->merge, 8);
     mbar_init(&x->merged, 8);
+    mbar_init(&x->spoilt, 8);
     mbar_init(&x->drain, 1);
-    x->abort = 0;
+    x->abort = x->any_bad[0] = x->any_bad[1] = 0;
     fence_mbar_init();
     fence_async_smem();
   }
   if (warp == 1) tma_prefetch_map(&km);
   if (warp == 2) tma_prefetch_map(&vm);
   if (warp == 3 && a.q_box) tma_prefetch_map(&qm);
+  if (threadIdx.x >= 128 && threadIdx.x < 128 + 2 * CAS_BLK) x->bad[0][threadIdx.x - 128] = 0xFFFF;
   if (warp == 0) tm_alloc(&x->tmem, 512);
   tc_fence_before();
   __syncthreads();
@@ -955,7 +1032,8 @@ extern "C" int cas_paged_attn(const cas_paged_kv* kv, const cas_paged_batch* b, 
   CUtensorMap km, vm, qm{};
   if (!make_map(&km, kv, kv->k) || !make_map(&vm, kv, kv->v) || (a.q_box && !make_q_map(&qm, q, b->rows, n_q_heads, a.G)))
     return CAS_ERR_CUDA;
-  if (occupancy((const void*)paged_attn_kernel, kThreads, kSmem) < 1) return CAS_ERR_CUDA;
+  if (cudaFuncSetAttribute(paged_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
+    return CAS_ERR_CUDA;
   const cudaStream_t st = (cudaStream_t)stream;
   if (const int e = launch_k(paged_attn_kernel, grid, kThreads, kSmem, st, a, km, vm, qm)) return e;
   if (grid < 2) return CAS_OK;

@@ -229,6 +229,8 @@ ATTN = [  # chunks, lengths with the chunk, Hq, Hkv, page
     ([260, 255, 1], [260, 511, 1300], 8, 4, 64),
     ([2], [6000], 64, 1, 64),                    # 128 query rows of one token pair
     ([3], [700], 200, 1, 64),                    # more heads in a group than rows in a tile
+    ([1, 2, 0] * 100, [(37 * i) % 400 + 2 for i in range(300)], 4, 1, 16),  # several sequences a lane of the scheduler
+    ([300, 1, 0, 290, 400], [400, 30, 20, 290, 1000], 6, 2, 32),
 ]
 
 
@@ -247,6 +249,48 @@ def test_paged_attn_layouts(cas, case, layout):
 @pytest.mark.parametrize("case", [0, 3, 6, 7, 8, 12])
 def test_paged_attn_unused_slots_may_hold_anything(cas, case, spoil):
     check_attn(cas, *ATTN[case], seed=case, spoil=spoil)
+
+
+@pytest.mark.parametrize("spoil", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("chunks,lens,Hq,page", [([5], [300], 8, 16), ([70], [70], 8, 32), ([200, 3], [500, 64], 12, 64),
+                                                 ([129, 1, 140], [257, 40, 140], 8, 128)])
+def test_paged_attn_values_that_a_row_does_not_see(cas, chunks, lens, Hq, page, spoil):
+    """Keys and values of later tokens of the chunk that are not finite: rows
+    before them are as without, rows from them on are not finite where the
+    values are not. Twice, so that nothing of the first call remains."""
+    Hkv = 2
+    starts, lens, table, n_pages, rows = batch(chunks, lens, page, seed=5)
+    k, v = pools(n_pages, page, Hkv, "tokens", seed=5)
+    q = torch.randn(rows, Hq, D, device="cuda").to(BF)
+    args = dev32(starts, lens, table)
+    clean = cas.paged_attn(q, k, v, *args).view(BF)
+    hit = {}
+    for b, (c, n) in enumerate(zip(chunks, lens)):
+        for back, d in ((1, 3), (c // 2 + 1, 100), (c // 2 + 1, 127)):
+            p = n - back
+            if p > n - c:  # not the chunk's first token: some row does not see it
+                v[table[b][p // page], p % page, 1, d] = spoil
+                hit[b, d] = min(hit.get((b, d), n), p)
+    bad = cas.paged_attn(q, k, v, *args).view(BF)
+    sees = torch.zeros(rows, Hq, D, dtype=torch.bool, device="cuda")
+    for r, b, p in serving.rows_of(starts, lens):
+        for (s, d), first in hit.items():
+            if s == b and p >= first:
+                sees[r, Hq // Hkv:, d] = True
+    assert not torch.isfinite(bad[sees]).any()
+    assert torch.equal(bad[~sees], clean[~sees])
+    for (b, d), first in hit.items():  # and keys: a score that is not finite is seen only by later rows
+        v[table[b][first // page], first % page, 1, d] = 0.5
+    v2 = v.clone()
+    v2[~torch.isfinite(v2)] = 0.5
+    base = cas.paged_attn(q, k, v2, *args).view(BF)
+    p = lens[0] - 1
+    k[table[0][p // page], p % page, 0, 0] = spoil
+    got = cas.paged_attn(q, k, v2, *args).view(BF)
+    last = starts[1] - 1
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[last] = False
+    assert torch.equal(got[keep], base[keep])
 
 
 def test_paged_attn_bad_pages_read_as_zeros(cas):
