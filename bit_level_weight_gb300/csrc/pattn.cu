@@ -900,13 +900,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
   const int chunks = 32 / gridDim.y, items = cut.rows * chunks;
   int width = 4;  // threads side by side on items: a power of two
   while (width < items && width < kJoinThreads) width *= 2;
-  const int share = kJoinThreads / width, mine = threadIdx.x & (width - 1), sub = threadIdx.x / width;
+  const int share = min(kJoinThreads / width, cut.pieces), mine = threadIdx.x & (width - 1), sub = threadIdx.x / width;
   const int64_t size = (int64_t)a.piece_rows * kPieceFloats, half = (int64_t)CAS_BLK * a.piece_rows;
   const float* base = a.ws + (int64_t)2 * blockIdx.x * size;
   for (int i0 = 0; i0 < items; i0 += width) {
     const int i = i0 + mine, q = i / cut.rows, fr = i - q * cut.rows, c = blockIdx.y * chunks + q;
     Part p{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    if (i < items) {
+    if (i < items && sub < share) {
 #pragma unroll 4
       for (int k = sub; k < cut.pieces; k += share) {
         // the unit is the first of every CTA but, perhaps, the first one

@@ -500,8 +500,9 @@ int cas_qk_norm_rope(const void* qkv, int qkv_type, int rows, int n_q_heads, int
  * target has mass; as the target's nothing is accepted there and the next
  * token is -1. A drafted token outside 0..vocab-1 has ratio 0, a NaN u accepts
  * nothing, and u[b][gamma] outside [0, 1) takes the first or last token with
- * r > 0. Sums are exact to about 2^-40: results depend on neither the order
- * of additions nor the batch. Errors: CAS_ERR_INVALID for batch < 0 or above
+ * r > 0. The draw's sums are good to about 2^-35 and exact sums of its weights,
+ * so the same call gives the same tokens; ratios are fp32. Calls that may overlap
+ * on the GPU need a workspace each. Errors: CAS_ERR_INVALID for batch < 0 or above
  * 65535, gamma outside 0..64, vocab outside 1..2^31-1, a stride below vocab, a
  * temperature that is negative, NaN, infinite or positive but outside
  * [1e-6, 1e6], or a null pointer; CAS_ERR_BUFFER if the workspace is null,
@@ -566,7 +567,11 @@ int cas_paged_append(const cas_paged_kv* kv, const cas_paged_batch* b, const voi
  * tokens) and long chunks of a prompt may share a batch. GQA: head h reads kv
  * head h / (n_q_heads / n_kv_heads). q, o: bf16 [rows][n_q_heads][128]; fp32
  * scores, statistics and sums, probabilities rounded to bf16 for the tensor
- * cores. A row that sees no key is zero. Errors: CAS_ERR_INVALID for the
+ * cores. A row that sees no key is zero. Keys and values at positions that a
+ * row does not see never reach it, whatever they hold; one that it sees and
+ * that is not finite makes its output not finite (of a value: in that
+ * dimension). Calls that may overlap on the GPU need a workspace each. The
+ * same call gives the same bits. Errors: CAS_ERR_INVALID for the
  * descriptors as in cas_paged_append, n_q_heads not a multiple of n_kv_heads
  * or a null or misaligned q or o; CAS_ERR_BUFFER if the workspace is null, not
  * 16-byte aligned or smaller than cas_paged_attn_workspace_bytes;

@@ -369,6 +369,91 @@ def test_paged_graph_follows_the_batch_on_the_device(cas):
         assert ((o.view(BF).double() - ref).abs() <= tol).all()
 
 
+def test_paged_attn_shared_and_repeated_pages(cas):
+    """Two sequences share their first pages, and one holds a page twice."""
+    k, v = pools(20, 32, 2, "tokens", seed=3)
+    starts, lens, table = [0, 2, 40, 41], [70, 100, 128], [[4, 7, 9, 0], [4, 7, 11, 2], [5, 5, 6, 5]]
+    q = torch.randn(41, 8, D, device="cuda").to(BF)
+    out = cas.paged_attn(q, k, v, *dev32(starts, lens, table)).view(BF)
+    ref, mass = serving.paged_attn(q, k, v, starts, lens, table)
+    assert ((out.double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -12) * mass + 2.0 ** -8 * ref.abs() + 1e-6).all()
+
+
+def test_two_streams_at_once(cas):
+    """Calls on two streams, each with its own buffers and workspace (made by
+    the call), give what they give one after the other."""
+    k, v = pools(300, 64, 8, "tokens", seed=9)
+    jobs = []
+    for i, (chunks, lens) in enumerate((([1, 1, 1], [6000, 3000, 5000]), ([500], [4000]))):
+        starts, lens, table, _, rows = batch(chunks, lens, 64, seed=i)
+        q = torch.randn(rows, 32, D, device="cuda").to(BF)
+        jobs.append((q, k, v) + dev32(starts, lens, table))
+    t, d, x, u = (a.cuda() for a in spec_case(3, 4, 50000, 2, 1.0))
+    want = [cas.paged_attn(*j) for j in jobs] + [cas.spec_verify(t, d, x, u)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [[], [], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(cas.paged_attn(*jobs[i]) if i < 2 else cas.spec_verify(t, d, x, u))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i in (0, 1) for o in got[i])
+    assert all(torch.equal(a, b) for o in got[2] for a, b in zip(o, want[2]))
+    # and a stream given by name
+    out = cas.paged_attn(*jobs[0], stream=streams[0])
+    streams[0].synchronize()
+    assert torch.equal(out, want[0])
+
+
+def test_launch_overlap_keeps_the_results(cas):
+    """A chain of the operators with launches that may overlap, captured."""
+    Hq, Hkv, page = 16, 4, 32
+    k, v = pools(64, page, Hkv, "tokens", seed=4)
+    args = dev32([0, 3, 300], [300, 700], [list(range(30)), list(range(30, 60))])
+    qkv = torch.randn(300, 24 * D, device="cuda")
+    t, d, x, u = (a.cuda() for a in spec_case(2, 3, 30000, 6, 0.8))
+
+    def chain():
+        q = cas.paged_append(qkv, Hq, k, v, *args, theta=1e6)
+        o = cas.paged_attn(q, k, v, *args)
+        a = cas.qk_norm_rope(qkv, Hq, Hkv, pos0=5)
+        return (q, o, *a, *cas.spec_verify(t, d, x, u), *cas.spec_verify(t, None, x, None, temperature=0.0))
+    want = chain()
+    torch.cuda.synchronize()
+    cas.set_launch_overlap(True)
+    try:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            chain()
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = chain()
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+    finally:
+        cas.set_launch_overlap(False)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert cas.cas_device_status() == 0
+
+
+def test_misplaced_tensors_are_refused(cas):
+    k, v = pools(4, 16, 2, "tokens")
+    args = dev32([0, 2], [5], [[0, 1]])
+    q = torch.zeros(2, 4, D, dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="one device"):
+        cas.paged_attn(q, k.cpu(), v.cpu(), *args)
+    with pytest.raises(ValueError, match="contiguous"):
+        cas.paged_append(torch.zeros(2, 2048, device="cuda")[:, ::2], 4, k, v, *args)
+    with pytest.raises(cas.CasError):
+        cas.paged_attn(q, k, v, *args, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    wide = torch.zeros(2, 8, D, dtype=BF, device="cuda")[:, ::2]  # gathered by the call
+    assert torch.equal(cas.paged_attn(wide, k, v, *args), cas.paged_attn(q, k, v, *args))
+
+
 # ------------------------------------------------------------------ acceptance
 def spec_case(B, G, V, seed, temp, masked=False, spread=2.5):
     g = torch.Generator().manual_seed(seed)
