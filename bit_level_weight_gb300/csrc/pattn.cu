@@ -154,7 +154,7 @@ struct Line {
 // Warp-wide: the line's length, and the place of cell `c * per` on it (false
 // when the line is shorter). A lane adds up `each` neighbouring sequences; the
 // lane that holds the place has its sequences looked at again by the warp.
-__device__ bool find_place(const AttnArgs& a, int64_t c, int grid, Line& line, Place& p) {
+__device__ bool find_place(const AttnArgs& a, int64_t c, int grid, Line& line, Place& p, Seq& s) {
   const int lane = threadIdx.x & 31;
   const int each = (a.d.batch + 31) / 32;
   int64_t own = 0;
@@ -189,7 +189,7 @@ __device__ bool find_place(const AttnArgs& a, int64_t c, int grid, Line& line, P
   if (!hit || per_head <= 0) return false;  // not reached: the sequence lies in the lane's
   p.hk = (int)div64(left, per_head);
   left -= p.hk * per_head;
-  const Seq s = seq_of(a, p.b);
+  s = seq_of(a, p.b);
   const int nq = unit_count(s);
   for (int q0 = 0; q0 < nq; q0 += 32) {
     const int n = q0 + lane < nq ? unit_tiles(s, a, q0 + lane) + kUnitCells : 0;
@@ -279,7 +279,8 @@ __device__ void scheduler(const AttnArgs& a, const CUtensorMap* qm, uint8_t* q_s
   Place p;
   Unit w{};
   Cut cut{};
-  const bool any = find_place(a, blockIdx.x, gridDim.x, line, p);
+  Seq s;
+  const bool any = find_place(a, blockIdx.x, gridDim.x, line, p, s);
   if (!any) {
     if (lane == 0) {
       a.cuts[blockIdx.x] = cut;
@@ -290,7 +291,6 @@ __device__ void scheduler(const AttnArgs& a, const CUtensorMap* qm, uint8_t* q_s
     return;
   }
   int64_t left = min(line.per, line.total - (int64_t)blockIdx.x * line.per);
-  Seq s = seq_of(a, p.b);
   int cell = p.cell;
   uint32_t uses[2] = {0, 0};  // of the Q tiles
   uint32_t loads = 0;         // units whose Q was fetched by TMA
@@ -307,16 +307,16 @@ __device__ void scheduler(const AttnArgs& a, const CUtensorMap* qm, uint8_t* q_s
     left -= end - cell;
     const bool two = w.rows > kTile, tile_b = !two && (u & 1);
     w.flags = (w.n == all ? kWhole : 0) | (u == 0 ? kFirst : 0) | (tile_b ? kTileB : 0);
-    if (w.t0 == 0 && w.n > 0 && w.n < all) {  // the unit's first piece: its cut
-      cut.pieces = 1 + (int)div64(all - w.n + line.per - 1, line.per);
-      cut.start = w.start, cut.hk = w.hk, cut.f0 = w.f0, cut.rows = w.rows;
-      cut.first = u == 0 ? 0 : 1;
-    }
     const bool last = left <= kUnitCells;  // (a next unit's first cells hold no tile)
     if (last) w.flags |= kLast;
     if (!wait(&x->u_empty[u & 1], ((u >> 1) & 1) ^ 1, x)) break;
     if (lane == 0) x->unit[u & 1] = w;
     arrive_warp(&x->u_full[u & 1]);
+    if (w.t0 == 0 && w.n > 0 && w.n < all) {  // the unit's first piece: its cut
+      cut.pieces = 1 + (int)div64(all - w.n + line.per - 1, line.per);
+      cut.start = w.start, cut.hk = w.hk, cut.f0 = w.f0, cut.rows = w.rows;
+      cut.first = u == 0 ? 0 : 1;
+    }
     // Q: rows of 256 bytes in swizzled halves. Rows that the unit does not have
     // hold another sequence's or what was there: nothing of them is used.
     const int first = tile_b ? 1 : 0, count = two ? 2 : 1;
@@ -563,7 +563,9 @@ __device__ bool guard_values(const Unit& w, int turn, int key0, uint32_t item, u
   const int r = threadIdx.x & 127;
   if (!wait(&x->kv_full[item % kRing], (item / kRing) & 1, x)) return false;
   uint8_t* row = ring + (item % kRing) * kBuf + r * 128;
+  bool wrote = false;
   if (key0 + r >= w.kv_end) {
+    wrote = true;
 #pragma unroll
     for (int c = 0; c < 8; ++c)
       *reinterpret_cast<uint4*>(row + c * 16) = *reinterpret_cast<uint4*>(row + kHalf + c * 16) = make_uint4(0, 0, 0, 0);
@@ -579,6 +581,7 @@ __device__ bool guard_values(const Unit& w, int turn, int key0, uint32_t item, u
       }
     }
     if ((top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u) {
+      wrote = true;
       for (int d = 0; d < CAS_BLK; ++d) {
         uint16_t* p = reinterpret_cast<uint16_t*>(row + (d >> 6) * kHalf + ((((d >> 3) & 7) ^ (r & 7)) << 4)) + (d & 7);
         if ((*p & 0x7F80u) == 0x7F80u) {
@@ -594,7 +597,7 @@ __device__ bool guard_values(const Unit& w, int turn, int key0, uint32_t item, u
       }
     }
   }
-  fence_async_smem();
+  if (wrote) fence_async_smem();
   return true;
 }
 
@@ -619,6 +622,9 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
     const int step = two ? 1 : 2;
     for (int j = two ? 0 : slot; j < w.n; j += step) {
       const int key0 = (w.t0 + j) * kTile;
+      if ((slot == 0 || !two) && (key0 + kTile > w.kv_end || guards(w, key0))) {
+        if (!guard_values(w, u & 1, key0, 2 * (base + j) + 1, ring, x)) return;
+      }
       if (!wait(&x->s_full[slot], ns++ & 1, x)) return;
       tc_fence_after();
       if (busy) {
@@ -697,9 +703,6 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
         tm_wait_st();
       }
       ++done;
-      if ((slot == 0 || !two) && (key0 + kTile > w.kv_end || guards(w, key0))) {
-        if (!guard_values(w, u & 1, key0, 2 * (base + j) + 1, ring, x)) return;
-      }
       tc_fence_before();
       if (pending) {
         if (!wait(&x->merged, (nm - 1) & 1, x)) return;
