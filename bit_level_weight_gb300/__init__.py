@@ -730,17 +730,19 @@ def _qkv(t: torch.Tensor, n_q_heads: int, n_kv_heads: int, what: str) -> int:
     raise ValueError(f"{what}: qkv must be fp32 or bfloat16")
 
 
-def _gammas(gamma_q, gamma_k):
-    for g, what in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
-        if g is not None:
-            _is_bf16(g, (128,), what)
+def _gamma(g: torch.Tensor | None, index: int, what: str) -> int | None:
+    if g is None:
+        return None
+    _is_bf16(g, (128,), what)
+    return _raw(g, index)
 
 
-def _head_rows(t: torch.Tensor, heads: int, index: int, what: str) -> tuple[int, int]:
+def _head_rows(t: torch.Tensor, shape: tuple, index: int, what: str) -> tuple[int, int]:
     """Address and row stride of bf16 rows [rows][heads][128] that may lie in a larger buffer."""
+    _is_bf16(t, shape, what)
     if t.get_device() != index:
         raise ValueError(f"libcas takes device tensors of one device: got {t.device}")
-    rows = t.shape[0]
+    rows, heads, _ = shape
     if rows and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != 128)):
         raise ValueError(f"{what}: the heads of a row must be contiguous")
     return t.data_ptr(), t.stride(0) if rows > 1 else heads * 128
@@ -756,28 +758,30 @@ def qk_norm_rope(qkv: torch.Tensor, n_q_heads: int, n_kv_heads: int, gamma_q: to
     pos0 + row % rows_per_seq. Returns (q, k, v) bf16 bit patterns
     [rows][H][128]; k and v may be given as rows of larger buffers."""
     kind = _qkv(qkv, n_q_heads, n_kv_heads, "qk_norm_rope")
-    rows, dev = qkv.shape[0], qkv.device
-    _gammas(gamma_q, gamma_k)
-    if pos is not None:
+    rows, dev, i = qkv.shape[0], qkv.device, qkv.get_device()
+    gqp, gkp = _gamma(gamma_q, i, "gamma_q"), _gamma(gamma_k, i, "gamma_k")
+    if pos is None:
+        pp = None
+    else:
         _is_i32(pos, (rows,), "pos")
+        pp = _raw(pos, i)
+    ks = vs = n_kv_heads * 128
     if q is None:
         q = torch.empty((rows, n_q_heads, 128), dtype=torch.int16, device=dev)
     else:
         _is_bf16(q, (rows, n_q_heads, 128), "q")
     if k is None:
         k = torch.empty((rows, n_kv_heads, 128), dtype=torch.int16, device=dev)
+        kp = k.data_ptr()
     else:
-        _is_bf16(k, (rows, n_kv_heads, 128), "k")
+        kp, ks = _head_rows(k, (rows, n_kv_heads, 128), i, "k")
     if v is None:
         v = torch.empty((rows, n_kv_heads, 128), dtype=torch.int16, device=dev)
+        vp = v.data_ptr()
     else:
-        _is_bf16(v, (rows, n_kv_heads, 128), "v")
-    i = qkv.get_device()
-    kp, ks = _head_rows(k, n_kv_heads, i, "k")
-    vp, vs = _head_rows(v, n_kv_heads, i, "v")
-    _call(lib().cas_qk_norm_rope, "cas_qk_norm_rope", i, stream, _raw(qkv, i), kind, rows, n_q_heads, n_kv_heads,
-          _raw(gamma_q, i), _raw(gamma_k, i), eps, _raw(pos, i), pos0, rows_per_seq or max(rows, 1), theta,
-          _raw(q, i), kp, ks, vp, vs)
+        vp, vs = _head_rows(v, (rows, n_kv_heads, 128), i, "v")
+    _call((_lib or lib()).cas_qk_norm_rope, "cas_qk_norm_rope", i, stream, _raw(qkv, i), kind, rows, n_q_heads,
+          n_kv_heads, gqp, gkp, eps, pp, pos0, rows_per_seq or max(rows, 1), theta, _raw(q, i), kp, ks, vp, vs)
     return q, k, v
 
 
@@ -828,14 +832,14 @@ def paged_append(qkv: torch.Tensor, n_q_heads: int, k_pages: torch.Tensor, v_pag
         raise ValueError("k_pages: [n_pages][page_size][n_kv_heads][128] expected")
     kind = _qkv(qkv, n_q_heads, k_pages.shape[2], "paged_append")
     rows, i = qkv.shape[0], qkv.get_device()
-    _gammas(gamma_q, gamma_k)
+    gqp, gkp = _gamma(gamma_q, i, "gamma_q"), _gamma(gamma_k, i, "gamma_k")
     if q is None:
         q = torch.empty((rows, n_q_heads, 128), dtype=torch.int16, device=qkv.device)
     else:
         _is_bf16(q, (rows, n_q_heads, 128), "q")
     kv, b = _paged(rows, k_pages, v_pages, row_start, kv_len, pages, i)
-    _call(lib().cas_paged_append, "cas_paged_append", i, stream, ctypes.byref(kv), ctypes.byref(b), _raw(qkv, i), kind,
-          n_q_heads, _raw(gamma_q, i), _raw(gamma_k, i), eps, theta, _raw(q, i))
+    _call((_lib or lib()).cas_paged_append, "cas_paged_append", i, stream, ctypes.byref(kv), ctypes.byref(b),
+          _raw(qkv, i), kind, n_q_heads, gqp, gkp, eps, theta, _raw(q, i))
     return q
 
 
@@ -859,7 +863,7 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ro
         out = torch.empty((rows, Hq, 128), dtype=torch.int16, device=dev)
     else:
         _is_bf16(out, (rows, Hq, 128), "out")
-    L = lib()
+    L = _lib or lib()
     if workspace is None:
         workspace = torch.empty(L.cas_paged_attn_workspace_bytes(rows, Hq, kv.n_kv_heads), dtype=torch.uint8,
                                 device=dev)
@@ -909,7 +913,7 @@ def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, x: torch.Tenso
     n = torch.empty(B, dtype=torch.int32, device=dev)
     tokens = torch.empty((B, G + 1), dtype=torch.int32, device=dev)
     ratio = torch.empty((B, G), dtype=torch.float32, device=dev)
-    L = lib()
+    L = _lib or lib()
     if workspace is None:
         workspace = torch.empty(L.cas_spec_verify_workspace_bytes(B, G, V), dtype=torch.uint8, device=dev)
     _call(L.cas_spec_verify, "cas_spec_verify", i, stream, tp, ts, dp, ds, _raw(x, i), _raw(u, i), _raw(n_draft, i), B,
