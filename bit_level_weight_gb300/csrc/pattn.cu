@@ -30,6 +30,22 @@
 //   warp 3          finds the CTA's units and hands them to the others one
 //                   ahead, with their Q rows
 //
+// What bounds it (measured on GB300, 8 kv heads, 32 query heads):
+//   one token a sequence: the K and V stream. 61 sequences of up to 8K: 168 us
+//     for 1.0 GB = 6.0 TB/s, 88 % of the measured copy rate; one sequence of 32K:
+//     36 us for 134 MB, of which about 8 us are the way to the first tile (place
+//     on the line, page table, first TMA) and 4 us the join.
+//   long chunks: 2048 rows over 32K in 674-695 us = 1.53-1.59 PFLOP/s, 80 % of
+//     cuBLAS's burst rate on this GPU. A key tile takes 1.6 us where its four products
+//     need 1.05: a slot's chain S -> softmax (0.7 us) -> P V, S is longer than what
+//     the other slot hides, and tensor memory holds no third slot (2 x (128 S +
+//     128 O) columns are all 512). Tried and slower: P V in two halves behind two
+//     barriers (790 us), two threads a row in sixteen softmax warps (880 us), the
+//     exponentials ahead of the maximum (790 us): each puts more waits or
+//     instructions next to the issuing warp, whose products then lag.
+//   short ragged chunks: a change of units costs a slot about 3 us (last
+//     product, output, first scores), which kUnitCells weighs in.
+//
 // Every wait is bounded: one that gives up marks the CTA, whose warps then
 // leave their loops, and sets a status that cas_device_status reads.
 //
@@ -51,12 +67,13 @@ namespace {
 
 constexpr int kTile = 128;                 // keys a tile, rows a slot
 constexpr int kUnit = 2 * kTile;           // flat rows a unit
-constexpr int kRing = 5;                   // K / V buffers
+constexpr int kRing = 5;                   // K / V buffers: with two Q tiles all of the shared memory
 constexpr uint32_t kBuf = kTile * 256;     // bytes of a K or V tile
 constexpr uint32_t kHalf = kBuf / 2;       // 64 of the 128 dimensions
 constexpr int kThreads = 384;               // three warpgroups of 168 registers a thread at launch
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;  // 2 * 216 + 72 = 3 * 168: the softmax keeps a row of S
 constexpr int kUnitCells = 2;              // cells of the line for a change of units: about two tiles' time
+                                           // (1, 2, 3 of them: 104, 98, 98 us on five ragged prompts)
 constexpr int kMinCells = kUnitCells + 2;  // cells a CTA takes at least
 constexpr uint32_t kSpins = 1u << 20;
 constexpr int64_t kPieceFloats = kTile + 2;  // floats a row of a partial result: output, maximum, sum
