@@ -34,11 +34,13 @@ namespace cas {
 int gemv_wait_status(bool clear);
 int attn_wait_status(bool clear);
 int set_first_wait_spins(uint32_t spins);
+int set_attn_spins(uint32_t spins);
 void set_launch_overlap(bool on);
 }  // namespace cas
 
 extern "C" int cas_test_first_wait_spins(uint32_t spins) {
   if (cudaDeviceSynchronize() != cudaSuccess) return CAS_ERR_CUDA;
+  if (const int e = cas::set_attn_spins(spins == 0 ? 0 : 1u << 20)) return e;
   return cas::set_first_wait_spins(spins == 0xFFFFFFFFu ? cas::kSpinLimit : spins);
 }
 

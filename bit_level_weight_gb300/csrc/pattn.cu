@@ -75,10 +75,13 @@ constexpr int kRegsSoftmax = 216, kRegsOther = 72;  // 2 * 216 + 72 = 3 * 168: t
 constexpr int kUnitCells = 2;              // cells of the line for a change of units: about two tiles' time
                                            // (1, 2, 3 of them: 104, 98, 98 us on five ragged prompts)
 constexpr int kMinCells = kUnitCells + 2;  // cells a CTA takes at least
-constexpr uint32_t kSpins = 1u << 20;
+constexpr uint32_t kSpins = 1u << 20;        // polls of a wait
 constexpr int64_t kPieceFloats = kTile + 2;  // floats a row of a partial result: output, maximum, sum
 
 __device__ int g_attn_status = 0;
+// Polls of a wait before it gives up; 0 (tests) also hands out no units, so that
+// the waits for one run out.
+__constant__ uint32_t c_attn_spins = kSpins;
 
 struct AttnArgs {
   PagedDev d;
@@ -250,7 +253,7 @@ struct Aux {
 };
 
 __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t phase, volatile int* abort) {
-  for (uint32_t i = 0; i < kSpins; ++i) {
+  for (uint32_t i = 0; i < c_attn_spins; ++i) {
     if (mbar_try_wait(bar, phase)) return true;
     if ((i & 63) == 63 && *abort) return false;
   }
@@ -296,6 +299,10 @@ __device__ void scheduler(const AttnArgs& a, const CUtensorMap* qm, uint8_t* q_s
   Place p;
   Unit w{};
   Cut cut{};
+  if (c_attn_spins == 0) {
+    if (lane == 0) a.cuts[blockIdx.x] = cut;
+    return;
+  }
   Seq s;
   const bool any = find_place(a, blockIdx.x, gridDim.x, line, p, s);
   if (!any) {
@@ -1013,6 +1020,10 @@ int attn_wait_status(bool clear) {
     if (cudaMemcpyToSymbol(g_attn_status, &z, sizeof(z)) != cudaSuccess) return CAS_ERR_CUDA;
   }
   return s;
+}
+
+int set_attn_spins(uint32_t spins) {
+  return cudaMemcpyToSymbol(c_attn_spins, &spins, sizeof(spins)) == cudaSuccess ? CAS_OK : CAS_ERR_CUDA;
 }
 
 }  // namespace cas

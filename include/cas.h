@@ -120,8 +120,9 @@ int cas_device_status(void* stream);
  * cas_device_status), wait once more with the normal limit so the copy lands
  * before the block exits, and write no output. This sets the limit of that
  * first wait for later launches: 0 makes it give up at once, 0xFFFFFFFF
- * restores the normal limit. Synchronises the device; returns CAS_OK or
- * CAS_ERR_CUDA. */
+ * restores the normal limit. With 0, cas_paged_attn's warps also wait for work
+ * that is never handed out, give up, record CAS_ERR_TIMEOUT and write no
+ * output. Synchronises the device; returns CAS_OK or CAS_ERR_CUDA. */
 int cas_test_first_wait_spins(uint32_t spins);
 /* Launch overlap, process-wide, off by default. When on, the kernels of later
  * calls are launched with programmatic stream serialization: a kernel's

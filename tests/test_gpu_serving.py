@@ -440,6 +440,28 @@ def test_launch_overlap_keeps_the_results(cas):
     assert cas.cas_device_status() == 0
 
 
+def test_paged_attn_wait_that_runs_out_is_reported(cas):
+    """Waits for work that nobody hands out give up: a status, no output, and
+    the next call with the normal limit is right."""
+    k, v = pools(40, 32, 2, "tokens", seed=3)
+    starts, lens, table = [0, 2, 140], [70, 600], [list(range(19)), list(range(20, 39))]
+    args = dev32(starts, lens, table)
+    q = torch.randn(140, 8, D, device="cuda").to(BF)
+    want = cas.paged_attn(q, k, v, *args)
+    assert cas.cas_device_status() == 0
+    out = torch.full((140, 8, D), 5.0, dtype=BF, device="cuda")
+    try:
+        assert cas.lib().cas_test_first_wait_spins(0) == 0
+        cas.paged_attn(q, k, v, *args, out=out)
+        assert cas.cas_device_status() == -8
+        assert cas.cas_device_status() == 0  # read once, then clear
+    finally:
+        assert cas.lib().cas_test_first_wait_spins(0xFFFFFFFF) == 0
+    assert (out == 5).all()
+    assert torch.equal(cas.paged_attn(q, k, v, *args), want)
+    assert cas.cas_device_status() == 0
+
+
 def test_misplaced_tensors_are_refused(cas):
     k, v = pools(4, 16, 2, "tokens")
     args = dev32([0, 2], [5], [[0, 1]])
