@@ -885,9 +885,12 @@ def _logit_rows(t: torch.Tensor, batch: int, rows: int, vocab: int, i: int, what
         raise ValueError(f"libcas takes device tensors of one device: got {t.device}")
     sb, sr, sv = t.stride()
     step = sr if rows > 1 else sb if batch > 1 else vocab
-    if batch and rows and ((vocab > 1 and sv != 1) or (rows > 1 and batch > 1 and sb != rows * step)):
+    if not batch or not rows:
+        return t.data_ptr(), vocab
+    # (rows that overlap, as those of an expanded tensor, have no stride that the call takes)
+    if (vocab > 1 and sv != 1) or step < vocab or (rows > 1 and batch > 1 and sb != rows * step):
         raise ValueError(f"{what}: evenly spaced contiguous rows expected")
-    return t.data_ptr(), max(step, vocab)
+    return t.data_ptr(), step
 
 
 def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, x: torch.Tensor, u: torch.Tensor | None,

@@ -175,3 +175,16 @@ def test_spec_binding(kw, what):
     a = dict(target=torch.zeros(2, 4, 10), draft=torch.zeros(2, 3, 10), x=z(2, 3), u=torch.zeros(2, 4)) | kw
     with pytest.raises(ValueError, match=what):
         cas.spec_verify(**a)
+
+
+@pytest.mark.parametrize("B,G", [(1, 3), (2, 0), (2, 3)])
+def test_spec_binding_refuses_expanded_rows(B, G):
+    """Rows that share memory have a stride below the vocabulary: read at any
+    other stride they would run past the tensor's end."""
+    a = dict(draft=torch.zeros(B, G, 10), x=z(B, G), u=torch.zeros(B, G + 1))
+    with pytest.raises(ValueError, match="evenly spaced"):
+        cas.spec_verify(torch.zeros(1, 1, 10).expand(B, G + 1, 10), **a)
+    if G > 1 or B > 1 and G:
+        a["draft"] = torch.zeros(1, 1, 10).expand(B, G, 10)
+        with pytest.raises(ValueError, match="evenly spaced"):
+            cas.spec_verify(torch.zeros(B, G + 1, 10), **a)
