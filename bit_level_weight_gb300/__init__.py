@@ -692,11 +692,11 @@ def _raw(t: torch.Tensor | None, index: int) -> int | None:
     return t.data_ptr()
 
 
-def _call(fn, what: str, index: int, stream, *args):
-    """Calls a C entry point on device `index` and its current (or the given) stream."""
+def _call(fn, what: str, index: int, *args):
+    """Calls a C entry point on device `index` and its current stream."""
     if index < 0:
         raise ValueError("libcas takes device tensors")
-    st = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    st = torch._C._cuda_getCurrentRawStream(index)
     if torch._C._cuda_getDevice() == index:
         status = fn(*args, st)
     else:
@@ -704,6 +704,16 @@ def _call(fn, what: str, index: int, stream, *args):
             status = fn(*args, st)
     if status != CAS_OK:
         raise CasError(status, what)
+
+
+def _with_stream(stream, t: torch.Tensor, fn, *args):
+    """fn(*args) with `stream` current: buffers that it makes, results among
+    them, come from that stream's memory, so that no other stream reuses them
+    under a kernel, and copies that it makes are ordered with the kernel."""
+    if not t.is_cuda or stream.device != t.device:
+        raise ValueError(f"libcas takes device tensors of the stream's device: got {t.device}")
+    with torch.cuda.stream(stream):
+        return fn(*args)
 
 
 def _is_bf16(t: torch.Tensor, shape: tuple, what: str):
@@ -757,6 +767,9 @@ def qk_norm_rope(qkv: torch.Tensor, n_q_heads: int, n_kv_heads: int, gamma_q: to
     no norm). qkv: fp32 or bfloat16 [rows][(Hq+2Hkv)*128]; pos: int32 [rows], or
     pos0 + row % rows_per_seq. Returns (q, k, v) bf16 bit patterns
     [rows][H][128]; k and v may be given as rows of larger buffers."""
+    if stream is not None:
+        return _with_stream(stream, qkv, qk_norm_rope, qkv, n_q_heads, n_kv_heads, gamma_q, gamma_k, eps, pos, pos0,
+                            rows_per_seq, theta, q, k, v)
     kind = _qkv(qkv, n_q_heads, n_kv_heads, "qk_norm_rope")
     rows, dev, i = qkv.shape[0], qkv.device, qkv.get_device()
     gqp, gkp = _gamma(gamma_q, i, "gamma_q"), _gamma(gamma_k, i, "gamma_k")
@@ -780,7 +793,7 @@ def qk_norm_rope(qkv: torch.Tensor, n_q_heads: int, n_kv_heads: int, gamma_q: to
         vp = v.data_ptr()
     else:
         vp, vs = _head_rows(v, (rows, n_kv_heads, 128), i, "v")
-    _call((_lib or lib()).cas_qk_norm_rope, "cas_qk_norm_rope", i, stream, _raw(qkv, i), kind, rows, n_q_heads,
+    _call((_lib or lib()).cas_qk_norm_rope, "cas_qk_norm_rope", i, _raw(qkv, i), kind, rows, n_q_heads,
           n_kv_heads, gqp, gkp, eps, pp, pos0, rows_per_seq or max(rows, 1), theta, _raw(q, i), kp, ks, vp, vs)
     return q, k, v
 
@@ -828,6 +841,9 @@ def paged_append(qkv: torch.Tensor, n_q_heads: int, k_pages: torch.Tensor, v_pag
     batch and writes its keys and values into their cache slots; returns q
     bf16 bit patterns [rows][n_q_heads][128]. Sequence b has the rows
     row_start[b] to row_start[b + 1] - 1, the last of its kv_len[b] tokens."""
+    if stream is not None:
+        return _with_stream(stream, qkv, paged_append, qkv, n_q_heads, k_pages, v_pages, row_start, kv_len, pages,
+                            gamma_q, gamma_k, eps, theta, q)
     if k_pages.dim() != 4:
         raise ValueError("k_pages: [n_pages][page_size][n_kv_heads][128] expected")
     kind = _qkv(qkv, n_q_heads, k_pages.shape[2], "paged_append")
@@ -838,7 +854,7 @@ def paged_append(qkv: torch.Tensor, n_q_heads: int, k_pages: torch.Tensor, v_pag
     else:
         _is_bf16(q, (rows, n_q_heads, 128), "q")
     kv, b = _paged(rows, k_pages, v_pages, row_start, kv_len, pages, i)
-    _call((_lib or lib()).cas_paged_append, "cas_paged_append", i, stream, ctypes.byref(kv), ctypes.byref(b),
+    _call((_lib or lib()).cas_paged_append, "cas_paged_append", i, ctypes.byref(kv), ctypes.byref(b),
           _raw(qkv, i), kind, n_q_heads, gqp, gkp, eps, theta, _raw(q, i))
     return q
 
@@ -852,6 +868,8 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ro
                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """q [rows][Hq][128] -> o bf16 bit patterns [rows][Hq][128] over the paged
     cache: every row sees its sequence's positions up to its own."""
+    if stream is not None:
+        return _with_stream(stream, q, paged_attn, q, k_pages, v_pages, row_start, kv_len, pages, out, workspace)
     if q.dim() != 3:
         raise ValueError("q: [rows][n_q_heads][128] expected")
     rows, Hq, _ = q.shape
@@ -867,7 +885,7 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ro
     if workspace is None:
         workspace = torch.empty(L.cas_paged_attn_workspace_bytes(rows, Hq, kv.n_kv_heads), dtype=torch.uint8,
                                 device=dev)
-    _call(L.cas_paged_attn, "cas_paged_attn", i, stream, ctypes.byref(kv), ctypes.byref(b), _raw(q, i), Hq,
+    _call(L.cas_paged_attn, "cas_paged_attn", i, ctypes.byref(kv), ctypes.byref(b), _raw(q, i), Hq,
           _raw(out, i), _raw(workspace, i), workspace.numel() * workspace.element_size())
     return out
 
@@ -901,6 +919,8 @@ def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, x: torch.Tenso
     numbers u [B][gamma + 1]. Returns (n_accepted int32 [B], tokens int32
     [B][gamma + 1]: the accepted, the next and -1 behind, ratio fp32
     [B][gamma]). temperature 0 is greedy; draft and u may then be None."""
+    if stream is not None:
+        return _with_stream(stream, x, spec_verify, target, draft, x, u, n_draft, temperature, workspace)
     if x.dtype != torch.int32 or x.dim() != 2:
         raise ValueError("spec_verify: x must be int32 [batch][gamma]")
     B, G = x.shape
@@ -919,7 +939,7 @@ def spec_verify(target: torch.Tensor, draft: torch.Tensor | None, x: torch.Tenso
     L = _lib or lib()
     if workspace is None:
         workspace = torch.empty(L.cas_spec_verify_workspace_bytes(B, G, V), dtype=torch.uint8, device=dev)
-    _call(L.cas_spec_verify, "cas_spec_verify", i, stream, tp, ts, dp, ds, _raw(x, i), _raw(u, i), _raw(n_draft, i), B,
+    _call(L.cas_spec_verify, "cas_spec_verify", i, tp, ts, dp, ds, _raw(x, i), _raw(u, i), _raw(n_draft, i), B,
           G, V, temperature, n.data_ptr(), tokens.data_ptr(), ratio.data_ptr(), _raw(workspace, i),
           workspace.numel() * workspace.element_size())
     return n, tokens, ratio

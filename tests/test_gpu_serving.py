@@ -406,6 +406,36 @@ def test_two_streams_at_once(cas):
     assert torch.equal(out, want[0])
 
 
+def test_named_stream_orders_copies_and_buffers(cas, monkeypatch):
+    """With a stream given, what the call copies and allocates belongs to it:
+    the current stream is busy meanwhile, and its memory is not taken."""
+    k, v = pools(20, 32, 2, "tokens", seed=7)
+    args = dev32([0, 2, 40], [70, 500], [list(range(3)) + [0] * 13, list(range(3, 19))])
+    wide = torch.randn(40, 16, D, device="cuda").to(BF)[:, ::2]  # gathered by the call
+    qkv = torch.randn(40, 12 * D, device="cuda")
+    t, d, x, u = (a.cuda() for a in spec_case(2, 3, 3000, 6, 0.8))
+    side = torch.cuda.Stream()
+
+    def run(**kw):
+        a = cas.qk_norm_rope(qkv, 8, 2, **kw)
+        return (cas.paged_attn(wide, k, v, *args, **kw), *a, cas.paged_append(qkv, 8, k.clone(), v.clone(), *args, **kw),
+                *cas.spec_verify(t, d, x, u, **kw))
+    want = run()
+    torch.cuda.synchronize()
+    seen, empty = [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: (seen.append(torch.cuda.current_stream()), empty(*a, **kw))[1])
+    kc, vc = k.clone(), v.clone()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # about 0.1 s
+    got = (cas.paged_attn(wide, k, v, *args, stream=side), *cas.qk_norm_rope(qkv, 8, 2, stream=side),
+           cas.paged_append(qkv, 8, kc, vc, *args, stream=side), *cas.spec_verify(t, d, x, u, stream=side))
+    side.synchronize()
+    monkeypatch.undo()
+    assert len(seen) >= 10 and all(s == side for s in seen)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_launch_overlap_keeps_the_results(cas):
     """A chain of the operators with launches that may overlap, captured."""
     Hq, Hkv, page = 16, 4, 32
