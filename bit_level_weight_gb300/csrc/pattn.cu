@@ -804,7 +804,7 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
       if (spoilt && mine) {
 #pragma unroll 1
         for (int d = 32 * c0; d < 32 * c1; ++d)
-          if (lim - w.first_pos >= (int)x->bad[u & 1][d]) {
+          if (lim >= 0 && lim - w.first_pos >= (int)x->bad[u & 1][d]) {
             if (whole)
               out[d] = 0x7FC0;
             else

@@ -293,6 +293,21 @@ def test_paged_attn_values_that_a_row_does_not_see(cas, chunks, lens, Hq, page, 
     assert torch.equal(got[keep], base[keep])
 
 
+def test_paged_attn_rows_far_before_the_first_token(cas):
+    """A length below the chunk's: the rows before position 0 see no key and are
+    zero, also those more than 2^16 before values that are not finite."""
+    rows, n = 70000, 3
+    k, v = pools(1, 16, 1, "tokens", seed=6)
+    q = torch.randn(rows, 1, D, device="cuda").to(BF)
+    v[0, 0, 0, 5] = float("nan")
+    out = cas.paged_attn(q, k, v, *dev32([0, rows], [n], [[0]])).view(BF)
+    assert (out[:rows - n] == 0).all()
+    assert out[rows - n:, 0, 5].isnan().all()
+    rest = out[rows - n:, 0].clone()
+    rest[:, 5] = 0
+    assert torch.isfinite(rest).all()
+
+
 def test_paged_attn_bad_pages_read_as_zeros(cas):
     def edit(table, n_pages):
         table[0][1], table[0][2], table[1][0] = n_pages, -1, 2 ** 31 - 1
