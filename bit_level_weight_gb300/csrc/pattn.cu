@@ -252,8 +252,9 @@ struct Aux {
   float m[2][kTile], l[2][kTile];
 };
 
-__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t phase, volatile int* abort) {
-  for (uint32_t i = 0; i < c_attn_spins; ++i) {
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t phase, volatile int* abort, uint64_t tiles) {
+  const uint64_t limit = c_attn_spins * tiles;
+  for (uint64_t i = 0; i < limit; ++i) {
     if (mbar_try_wait(bar, phase)) return true;
     if ((i & 63) == 63 && *abort) return false;
   }
@@ -261,10 +262,11 @@ __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t phase, volatil
   atomicExch(&g_attn_status, CAS_ERR_TIMEOUT);
   return false;
 }
-// Warp-wide; false when any lane gave up.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t phase, Aux* x) {
+// Warp-wide; false when any lane gave up. tiles: what the wait may have to
+// outlast, a few for all but the scheduler's, which lie behind whole units.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t phase, Aux* x, uint64_t tiles = 1) {
   bool ok = mbar_try_wait(bar, phase);
-  if (!__all_sync(CAS_FULL, ok)) ok = ok || wait_long(bar, phase, &x->abort);
+  if (!__all_sync(CAS_FULL, ok)) ok = ok || wait_long(bar, phase, &x->abort, tiles);
   return __all_sync(CAS_FULL, ok);
 }
 __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
@@ -317,6 +319,7 @@ __device__ void scheduler(const AttnArgs& a, const CUtensorMap* qm, uint8_t* q_s
   int64_t left = min(line.per, line.total - (int64_t)blockIdx.x * line.per);
   int cell = p.cell;
   uint32_t uses[2] = {0, 0};  // of the Q tiles
+  uint64_t handed = 1;        // tiles of the units so far: the limit of the waits grows with them
   uint32_t loads = 0;         // units whose Q was fetched by TMA
   for (uint32_t u = 0;; ++u) {
     const int all = unit_tiles(s, a, p.qt);
@@ -333,7 +336,7 @@ __device__ void scheduler(const AttnArgs& a, const CUtensorMap* qm, uint8_t* q_s
     w.flags = (w.n == all ? kWhole : 0) | (u == 0 ? kFirst : 0) | (tile_b ? kTileB : 0);
     const bool last = left <= kUnitCells;  // (a next unit's first cells hold no tile)
     if (last) w.flags |= kLast;
-    if (!wait(&x->u_empty[u & 1], ((u >> 1) & 1) ^ 1, x)) break;
+    if (!wait(&x->u_empty[u & 1], ((u >> 1) & 1) ^ 1, x, handed)) break;
     if (lane == 0) x->unit[u & 1] = w;
     arrive_warp(&x->u_full[u & 1]);
     if (w.t0 == 0 && w.n > 0 && w.n < all) {  // the unit's first piece: its cut
@@ -345,8 +348,9 @@ __device__ void scheduler(const AttnArgs& a, const CUtensorMap* qm, uint8_t* q_s
     // hold another sequence's or what was there: nothing of them is used.
     const int first = tile_b ? 1 : 0, count = two ? 2 : 1;
     bool ok = true;
-    for (int t = first; t < first + count; ++t) ok = ok && wait(&x->q_empty[t], (uses[t]++ & 1) ^ 1, x);
+    for (int t = first; t < first + count; ++t) ok = ok && wait(&x->q_empty[t], (uses[t]++ & 1) ^ 1, x, handed);
     if (!ok) break;
+    handed += w.n;
     if (a.q_box) {  // boxes of the group's heads x 128 / G tokens
       if (lane == 0) {
         mbar_arrive_tx(&x->q_full[u & 1], count * kBuf);

@@ -327,6 +327,35 @@ def test_paged_attn_long_context_large_scores(cas):
     check_attn(cas, [2, 40], [20000, 9001], 8, 2, 64, scale=8.0)
 
 
+def test_paged_attn_long_units(cas):
+    """Units of 32768 key tiles, two a CTA (every page of the table is the same
+    one): no wait gives up, however long a unit takes.
+
+    The page's tokens at positions up to p count (p - s) // 1024 + 1 times each.
+    Tolerance: rounding of P and of the output as elsewhere, and fp32 sums of n
+    terms in turn, at most n 2^-23 of their absolute sum where each addition may
+    be cut instead of rounded: 8 products of 16 keys a tile for the output
+    (2^18 additions), one a tile for the sum (2^15)."""
+    page, n, T, G = 1024, 1 << 22, 19456, 4
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k = torch.randn(1, page, 1, D, generator=g, device="cuda").to(BF)
+    v = (1 + torch.randn(1, page, 1, D, generator=g, device="cuda")).to(BF)
+    q = torch.randn(T, G, D, generator=g, device="cuda").to(BF)
+    out = torch.full((T, G, D), 5.0, dtype=BF, device="cuda")
+    cas.paged_attn(q, k, v, *dev32([0, T], [n], [[0] * (n // page)]), out=out)
+    assert cas.cas_device_status() == 0
+    pick = torch.tensor([0, 1, 63, 64, 5000, 9727, 9728, 15000, T - 2, T - 1], device="cuda")
+    pos = n - T + pick
+    count = (pos[:, None] - torch.arange(page, device="cuda")) // page + 1
+    s = q[pick].double() @ k[0, :, 0].double().T / D ** 0.5
+    w = torch.softmax(s + count[:, None, :].double().log(), -1)
+    ref, mass = w @ v[0, :, 0].double(), w @ v[0, :, 0].double().abs()
+    err = (out[pick].double() - ref).abs()
+    tol = (2.0 ** -8 + 2.0 ** -12 + 2.0 ** 18 * 2.0 ** -23) * mass + (2.0 ** -8 + 2.0 ** 15 * 2.0 ** -23) * ref.abs()
+    print("worst", (err / mass).max().item())
+    assert (err <= tol).all(), f"worst {(err / tol).max().item():.3g}"
+
+
 def test_paged_attn_offsets_beyond_32_bits(cas):
     """Pages whose element offsets pass 2^32 in a pool that is mostly unused."""
     H, page = 8, 64
