@@ -794,7 +794,8 @@ def qk_norm_rope(qkv: torch.Tensor, n_q_heads: int, n_kv_heads: int, gamma_q: to
     else:
         vp, vs = _head_rows(v, (rows, n_kv_heads, 128), i, "v")
     _call((_lib or lib()).cas_qk_norm_rope, "cas_qk_norm_rope", i, _raw(qkv, i), kind, rows, n_q_heads,
-          n_kv_heads, gqp, gkp, eps, pp, pos0, rows_per_seq or max(rows, 1), theta, _raw(q, i), kp, ks, vp, vs)
+          n_kv_heads, gqp, gkp, eps, pp, pos0, max(rows, 1) if rows_per_seq is None else rows_per_seq, theta,
+          _raw(q, i), kp, ks, vp, vs)
     return q, k, v
 
 

@@ -148,9 +148,10 @@ __device__ __forceinline__ int64_t head_cells(const AttnArgs& a, int b, int lane
     const int bb = __shfl_sync(CAS_FULL, b, src);
     const Seq t = seq_of(a, bb);
     const int n = unit_count(t);
-    int part = 0;
+    int64_t part = 0;
     for (int i = lane; i < n; i += 32) part += unit_tiles(t, a, i) + kUnitCells;
-    part = warp_sum(part);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(CAS_FULL, part, d);
     if (lane == src) sum = part;
   }
   return sum;
@@ -1035,6 +1036,7 @@ int set_attn_spins(uint32_t spins) {
 using namespace cas;
 
 extern "C" uint64_t cas_paged_attn_workspace_bytes(int rows, int n_q_heads, int n_kv_heads) {
+  if (rows < 1 || n_q_heads < 1 || n_kv_heads < 1) return 16;
   const int64_t g = sm_count();
   return ((uint64_t)g * sizeof(Cut) + 255) / 256 * 256 + 2 * g * piece_rows(rows, n_q_heads, n_kv_heads) * kPieceFloats * 4;
 }

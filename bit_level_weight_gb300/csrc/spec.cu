@@ -14,7 +14,7 @@
 // depend on the order of additions. So the rows that the draw uses are taken in
 // more than fp32:
 //   - exponentials to about 2^-37: y = logit * log2(e) / T as two floats, split
-//     into n + j / 32 + g with |g| <= 1 / 64; 2^(j/32) from a table of two
+//     into n + j / 32 + g with |g| <= 1 / 64 (table-driven, after P. Tang, 1989); 2^(j/32) from a table of two
 //     floats, 2^g - 1 = g ln 2 (two floats) + a short polynomial (fp32, below
 //     2^-14 of the value); two logits at a time in packed arithmetic. fp64 has
 //     2 lanes a SM and clock: 30 operations of it cost a row more than reading it;
@@ -679,7 +679,7 @@ Plan plan_of(int batch, int gamma, int64_t vocab, bool greedy) {
 }  // namespace
 
 extern "C" uint64_t cas_spec_verify_workspace_bytes(int batch, int gamma, int64_t vocab) {
-  if (batch < 1 || gamma < 0 || vocab < 1) return 16;
+  if (batch < 1 || batch > 65535 || gamma < 0 || gamma > kMaxGamma || vocab < 1 || vocab > 0x7FFFFFFF) return 16;
   return std::max(plan_of(batch, gamma, vocab, false).bytes, plan_of(batch, gamma, vocab, true).bytes);
 }
 

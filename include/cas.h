@@ -513,6 +513,7 @@ int cas_spec_verify(const float* target, int64_t target_stride, const float* dra
                     const int32_t* x, const float* u, const int32_t* n_draft, int batch, int gamma, int64_t vocab,
                     double temperature, int32_t* n_accepted, int32_t* tokens, float* ratio, void* workspace,
                     uint64_t workspace_bytes, void* stream);
+/* Workspace bytes of cas_spec_verify (16 for sizes that it refuses). */
 uint64_t cas_spec_verify_workspace_bytes(int batch, int gamma, int64_t vocab);
 
 /* ------------------------------------------------------------------ paged cache
@@ -579,6 +580,7 @@ int cas_paged_append(const cas_paged_kv* kv, const cas_paged_batch* b, const voi
  * CAS_ERR_CUDA. rows = 0 or batch = 0 does nothing. */
 int cas_paged_attn(const cas_paged_kv* kv, const cas_paged_batch* b, const uint16_t* q, int n_q_heads, uint16_t* o,
                    void* workspace, uint64_t workspace_bytes, void* stream);
+/* Workspace bytes of cas_paged_attn (16 for sizes that it refuses). */
 uint64_t cas_paged_attn_workspace_bytes(int rows, int n_q_heads, int n_kv_heads);
 
 #ifdef __cplusplus

@@ -188,3 +188,11 @@ def test_spec_binding_refuses_expanded_rows(B, G):
         a["draft"] = torch.zeros(1, 1, 10).expand(B, G, 10)
         with pytest.raises(ValueError, match="evenly spaced"):
             cas.spec_verify(torch.zeros(B, G + 1, 10), **a)
+
+
+def test_workspace_bytes_of_refused_sizes(L):
+    for rows, hq, hkv in ((-1, 4, 2), (0, 4, 2), (2, 0, 2), (2, -8, 2), (2, 4, 0), (2, 4, -1)):
+        assert L.cas_paged_attn_workspace_bytes(rows, hq, hkv) == 16
+    for b, g, n in ((0, 3, 10), (65536, 3, 10), (2, 65, 10), (2, -1, 10), (2, 3, 0), (2, 3, 1 << 31)):
+        assert L.cas_spec_verify_workspace_bytes(b, g, n) == 16
+    assert L.cas_paged_attn_workspace_bytes(1, 4, 2) > 1000 and L.cas_spec_verify_workspace_bytes(65535, 64, 10) > 1 << 20
