@@ -31,12 +31,13 @@
 //                   ahead, with their Q rows
 //
 // What bounds it (measured on GB300, 8 kv heads, 32 query heads):
-//   one token a sequence: the K and V stream. 61 sequences of up to 8K: 168 us
-//     for 1.0 GB = 6.0 TB/s, 88 % of the measured copy rate; one sequence of 32K:
-//     36 us for 134 MB, of which about 8 us are the way to the first tile (place
+//   one token a sequence: the K and V stream. 61 sequences of up to 8K: 166-171
+//     us for 1.0 GB = 5.8-6.0 TB/s, 86-88 % of the measured copy rate; one sequence of 32K:
+//     36-38 us for 134 MB, of which about 8 us are the way to the first tile (place
 //     on the line, page table, first TMA) and 4 us the join.
-//   long chunks: 2048 rows over 32K in 674-695 us = 1.53-1.59 PFLOP/s, 80 % of
-//     cuBLAS's burst rate on this GPU. A key tile takes 1.6 us where its four products
+//   long chunks: 2048 rows over 32K in 674-703 us = 1.52-1.58 PFLOP/s, about
+//     80 % of cuBLAS's burst rate on this GPU (738 us in long runs, where the power
+//     cap holds the SMs at 1890 MHz). A key tile takes 1.6 us where its four products
 //     need 1.05: a slot's chain S -> softmax (0.7 us) -> P V, S is longer than what
 //     the other slot hides, and tensor memory holds no third slot (2 x (128 S +
 //     128 O) columns are all 512). Tried and slower: P V in two halves behind two
@@ -51,7 +52,9 @@
 //
 // Rounding: scores, statistics and sums are fp32; P is rounded to bf16 for the
 // product with V (2^-8 relative each, the size of the output's own rounding),
-// the sum takes it unrounded.
+// the sum takes it unrounded. The tensor cores cut their sums: measured on units
+// that one CTA takes whole, the output is 0.05 % small at 128K tokens, 0.33 % at
+// 1M, 1.5 % at 4M; spread over the GPU, one token over 4M shows nothing of it.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
