@@ -52,8 +52,8 @@
 //
 // Rounding: scores, statistics and sums are fp32; P is rounded to bf16 for the
 // product with V (2^-8 relative each, the size of the output's own rounding),
-// the sum takes it unrounded. The tensor cores cut their sums: measured on units
-// that one CTA takes whole, the output is 0.05 % small at 128K tokens, 0.33 % at
+// the sum takes it unrounded. Measured on units that one CTA takes whole (as
+// if the tensor cores cut their sums instead of rounding them), the output is 0.05 % small at 128K tokens, 0.33 % at
 // 1M, 1.5 % at 4M; spread over the GPU, one token over 4M shows nothing of it.
 #include <cuda.h>
 #include <cuda_bf16.h>
