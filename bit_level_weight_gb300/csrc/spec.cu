@@ -22,10 +22,10 @@
 //     the remainder is P sum(Q) - Q sum(P) by its upper halves, without division.
 //
 // What bounds it: one sequence of 4 drafts over 128256 tokens, three launches and
-// their dependent loads (20 us for 4.6 MB); 29 sequences of up to 6 drafts over
-// 151936, the stats at 4.8 TB/s (24 us for 114 MB) and then instruction issue:
-// about 50 instructions a weight, 36 us and 34 us for the sums and the rest
-// (83 us together). Tried: fp64 (320 us), one cluster of 16 CTAs a sequence
+// their dependent loads (18.5 us for 4.6 MB); 29 sequences of up to 6 drafts over
+// 151936 tokens take 76 us: the stats at 4.8 TB/s (24 us for 114 MB), then the
+// arithmetic of the sums and the rest, about 50 instructions a weight, with the
+// logits loaded ahead of it. Tried: fp64 (320 us), one cluster of 16 CTAs a sequence
 // (185 us), weights kept as pairs of floats to the end (84 us), a table of 1024
 // steps and a shorter polynomial (81 us, but 22.5 us for the single sequence).
 #include <cuda_runtime.h>
@@ -43,6 +43,8 @@ namespace {
 constexpr int kStatThreads = 256;
 constexpr int kThreads = 256;  // of the sums and the rest
 constexpr int kMaxGamma = 64;
+constexpr int kAhead = 4;  // tokens of a row that a thread loads before it weighs the ones in hand: 29 sequences
+                           // of up to 6 drafts over 151936 tokens took 83 us without, 77.5 with 2, 76 with 4
 
 struct SpecArgs {
   const float *target, *draft, *u;
@@ -456,16 +458,30 @@ __global__ void __launch_bounds__(kThreads) sums_kernel(SpecArgs a) {
   const int64_t i0 = blockIdx.y * a.per, i1 = min(a.V, i0 + a.per);
   uint64_t tp = 0, tq = 0;
   if (!wp.none) {
-#pragma unroll 2
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += 2 * kThreads) {
-      const bool two = i + kThreads < i1;
+    auto load = [&](const float* row, int64_t i, float v[kAhead]) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) v[k] = i + k * kThreads < i1 ? __ldg(row + i + k * kThreads) : -INFINITY;
+    };
+    float p[kAhead], q[kAhead];
+    load(pr, i0 + threadIdx.x, p);
+    if (sub) load(qr, i0 + threadIdx.x, q);
+#pragma unroll 1
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kAhead * kThreads) {
+      float pn[kAhead], qn[kAhead];
+      load(pr, i + kAhead * kThreads, pn);
+      if (sub) load(qr, i + kAhead * kThreads, qn);
       uint64_t w[2];
-      weigh2(__ldg(pr + i), two ? __ldg(pr + i + kThreads) : -INFINITY, wp, a, table, w);
-      tp += w[0] + w[1];
-      if (sub) {
-        weigh2(__ldg(qr + i), two ? __ldg(qr + i + kThreads) : -INFINITY, wq, a, table, w);
-        tq += w[0] + w[1];
+#pragma unroll
+      for (int k = 0; k < kAhead; k += 2) {
+        weigh2(p[k], p[k + 1], wp, a, table, w);
+        tp += w[0] + w[1];
+        if (sub) {
+          weigh2(q[k], q[k + 1], wq, a, table, w);
+          tq += w[0] + w[1];
+        }
       }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) p[k] = pn[k], q[k] = qn[k];
     }
   }
   tp = block_sum64(tp, red);
@@ -534,13 +550,26 @@ __global__ void __launch_bounds__(kThreads) rest_kernel(SpecArgs a) {
     d.zq = zq << d.lq;
     const int64_t i0 = blockIdx.y * a.per, i1 = min(a.V, i0 + a.per);
     uint64_t t = 0;
-#pragma unroll 2
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += 2 * kThreads) {
-      const bool two = i + kThreads < i1;
-      uint64_t r[2];
-      d.get2(__ldg(d.pr + i), two ? __ldg(d.pr + i + kThreads) : -INFINITY, __ldg(d.qr + i),
-             two ? __ldg(d.qr + i + kThreads) : -INFINITY, a, table, r);
-      t += r[0] + r[1];
+    auto load = [&](const float* row, int64_t i, float v[kAhead]) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) v[k] = i + k * kThreads < i1 ? __ldg(row + i + k * kThreads) : -INFINITY;
+    };
+    float p[kAhead], q[kAhead];
+    load(d.pr, i0 + threadIdx.x, p);
+    load(d.qr, i0 + threadIdx.x, q);
+#pragma unroll 1
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kAhead * kThreads) {
+      float pn[kAhead], qn[kAhead];
+      load(d.pr, i + kAhead * kThreads, pn);
+      load(d.qr, i + kAhead * kThreads, qn);
+#pragma unroll
+      for (int k = 0; k < kAhead; k += 2) {
+        uint64_t r[2];
+        d.get2(p[k], p[k + 1], q[k], q[k + 1], a, table, r);
+        t += r[0] + r[1];
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) p[k] = pn[k], q[k] = qn[k];
     }
     t = block_sum64(t, red);
     if (threadIdx.x == 0) {
@@ -664,7 +693,8 @@ Plan plan_of(int batch, int gamma, int64_t vocab, bool greedy) {
   Plan p{};
   const int rows = batch * (greedy ? gamma + 1 : 2 * gamma + 1);
   slice(rows, vocab, &p.slices, &p.vecs);
-  // parts of the vocabulary: four tokens a thread at least, eight CTAs an SM wanted
+  // parts of the vocabulary: four tokens a thread at least, eight CTAs an SM wanted, since sequences differ in
+  // the rows that they sum (29 sequences: 108, 92, 78, 76, 83 us for 3, 4, 6, 8, 12; a single one the same)
   const int64_t want = std::max<int64_t>(1, (int64_t)sm_count() * 8 / batch);
   p.per = std::max<int64_t>(4 * kThreads, (vocab + want - 1) / want);
   p.per = std::max<int64_t>((p.per + 2 * kThreads - 1) / (2 * kThreads) * (2 * kThreads), (vocab + kMaxParts - 1) / kMaxParts);
