@@ -245,12 +245,17 @@ struct Aux {
   uint64_t kv_full[kRing], kv_empty[kRing];
   uint64_t u_full[2], u_empty[2], q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], o_full[2], merge, merged, spoilt, drain;
+  uint64_t seen[2];  // slot 1 is through with the marks below: of even, of odd units
   uint32_t tmem;
   int abort;
   Unit unit[2];
-  // values that are not finite and that not every row of the unit sees, for the
-  // unit at hand and the next (one slot may be ahead): whether there are any, and
-  // the first position for each dimension, counted from the unit's first row's
+  // values that are not finite and that not every row of the unit sees, for an
+  // even and an odd unit: whether there are any, and the first position for each
+  // dimension, counted from the unit's first row's. Slot 0 may be two units ahead
+  // of slot 1 (with one key tile, a unit's O of slot 0 is out before slot 1's P is
+  // waited for), but then waits for slot 1 in seen[u & 1] before it marks. Slot 1 is
+  // one ahead at most: its O of unit u, or the merge of the two, needs slot 0's P
+  // of u, which follows all that slot 0 does for u - 1.
   int any_bad[2];
   uint16_t bad[2][CAS_BLK];
   float m[2][kTile], l[2][kTile];
@@ -591,8 +596,9 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v, bool wide) {
 __device__ __forceinline__ bool guards(const Unit& w, int key0) {
   return min(key0 + kTile, w.kv_end) - 1 > w.first_pos;  // a token that the unit's first row does not see
 }
-__device__ bool guard_values(const Unit& w, int turn, int key0, uint32_t item, uint8_t* ring, Aux* x) {
-  const int r = threadIdx.x & 127;
+__device__ bool guard_values(const Unit& w, uint32_t u, int slot, int key0, uint32_t item, uint8_t* ring, Aux* x) {
+  const int r = threadIdx.x & 127, turn = u & 1;
+  if (slot == 0 && !wait(&x->seen[turn], ((u >> 1) & 1) ^ 1, x)) return false;  // of unit u - 2
   if (!wait(&x->kv_full[item % kRing], (item / kRing) & 1, x)) return false;
   uint8_t* row = ring + (item % kRing) * kBuf + r * 128;
   bool wrote = false;
@@ -655,7 +661,7 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
     for (int j = two ? 0 : slot; j < w.n; j += step) {
       const int key0 = (w.t0 + j) * kTile;
       if ((slot == 0 || !two) && (key0 + kTile > w.kv_end || guards(w, key0))) {
-        if (!guard_values(w, u & 1, key0, 2 * (base + j) + 1, ring, x)) return;
+        if (!guard_values(w, u, slot, key0, 2 * (base + j) + 1, ring, x)) return;
       }
       if (!wait(&x->s_full[slot], ns++ & 1, x)) return;
       tc_fence_after();
@@ -829,6 +835,7 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
       arrive_warp(&x->spoilt);
       if (!wait(&x->spoilt, nb++ & 1, x)) return;
     }
+    if (slot == 1) arrive_warp(&x->seen[u & 1]);
     if (!two) {  // both slots' O, m and l are read before either is written again
       arrive_warp(&x->merged);
       ++nm;
@@ -863,6 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&x->s_full[i], 1);
       mbar_init(&x->p_full[i], 4);
       mbar_init(&x->o_full[i], 1);
+      mbar_init(&x->seen[i], 4);
     }
     mbar_init(&x->merge, 8);
     mbar_init(&x->merged, 8);

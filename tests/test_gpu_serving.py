@@ -293,6 +293,27 @@ def test_paged_attn_values_that_a_row_does_not_see(cas, chunks, lens, Hq, page, 
     assert torch.equal(got[keep], base[keep])
 
 
+@pytest.mark.parametrize("chunks,deep", [([64] * 100, 0), ([48, 64] * 100, 500), ([1, 64, 33, 7, 64] * 40, 200)])
+def test_paged_attn_many_units_a_cta(cas, chunks, deep):
+    """Many short prompts: every CTA takes several units in a row, most of 129 to
+    256 rows and of a few key tiles. Then with values that only a sequence's last
+    row sees not finite, in every third sequence, several times."""
+    Hq, Hkv, page = 32, 8, 16
+    lens = [c + ((37 * i) % deep if deep else 0) for i, c in enumerate(chunks)]
+    q, k, v, starts, lens, table, out = check_attn(cas, chunks, lens, Hq, Hkv, page, seed=11)
+    args = dev32(starts, lens, table)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    for b in range(0, len(chunks), 3):
+        n, h, d = lens[b], b % Hkv, (7 * b) % D
+        v[table[b][(n - 1) // page], (n - 1) % page, h, d] = float("nan")
+        hit[starts[b + 1] - 1, 4 * h:4 * h + 4, d] = True
+    for _ in range(5):
+        got = cas.paged_attn(q, k, v, *args).view(BF)
+        assert got[hit].isnan().all()
+        assert torch.equal(got[~hit], out[~hit])
+    assert cas.cas_device_status() == 0
+
+
 def test_paged_attn_rows_far_before_the_first_token(cas):
     """A length below the chunk's: the rows before position 0 see no key and are
     zero, also those more than 2^16 before values that are not finite."""
