@@ -40,7 +40,7 @@ void set_launch_overlap(bool on);
 
 extern "C" int cas_test_first_wait_spins(uint32_t spins) {
   if (cudaDeviceSynchronize() != cudaSuccess) return CAS_ERR_CUDA;
-  if (const int e = cas::set_attn_spins(spins == 0 ? 0 : 1u << 20)) return e;
+  if (const int e = cas::set_attn_spins(spins <= 1 ? spins : 1u << 20)) return e;
   return cas::set_first_wait_spins(spins == 0xFFFFFFFFu ? cas::kSpinLimit : spins);
 }
 

@@ -48,7 +48,8 @@
 //     product, output, first scores), which kUnitCells weighs in.
 //
 // Every wait is bounded: one that gives up marks the CTA, whose warps then
-// leave their loops, and sets a status that cas_device_status reads.
+// leave their loops, and sets a status that cas_device_status reads. Units that
+// such a CTA holds a piece of are not joined.
 //
 // Rounding: scores, statistics and sums are fp32; P is rounded to bf16 for the
 // product with V (2^-8 relative each, the size of the output's own rounding),
@@ -83,8 +84,11 @@ constexpr int64_t kPieceFloats = kTile + 2;  // floats a row of a partial result
 
 __device__ int g_attn_status = 0;
 // Polls of a wait before it gives up; 0 (tests) also hands out no units, so that
-// the waits for one run out.
+// the waits for one run out. 1 (tests): so in every second CTA.
 __constant__ uint32_t c_attn_spins = kSpins;
+__device__ __forceinline__ uint32_t spins() {
+  return c_attn_spins == 1 ? (blockIdx.x & 1 ? 0 : kSpins) : c_attn_spins;
+}
 
 struct AttnArgs {
   PagedDev d;
@@ -100,6 +104,7 @@ struct AttnArgs {
 };
 struct Cut {
   int pieces;        // of the unit, CTAs c .. c + pieces - 1; 0: none
+  int ok;            // CTA c has written all its pieces
   int start, hk, f0, rows, first;  // first row of the sequence, kv head, flat rows; the first piece's place
 };
 __device__ __forceinline__ int div_g(const AttnArgs& a, int f) {
@@ -249,6 +254,7 @@ struct Aux {
   uint32_t tmem;
   int abort;
   Unit unit[2];
+  Cut cut;
   // values that are not finite and that not every row of the unit sees, for an
   // even and an odd unit: whether there are any, and the first position for each
   // dimension, counted from the unit's first row's. Slot 0 may be two units ahead
@@ -262,7 +268,7 @@ struct Aux {
 };
 
 __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t phase, volatile int* abort, uint64_t tiles) {
-  const uint64_t limit = c_attn_spins * tiles;
+  const uint64_t limit = spins() * tiles;
   for (uint64_t i = 0; i < limit; ++i) {
     if (mbar_try_wait(bar, phase)) return true;
     if ((i & 63) == 63 && *abort) return false;
@@ -309,16 +315,11 @@ __device__ void scheduler(const AttnArgs& a, const CUtensorMap* qm, uint8_t* q_s
   Line line;
   Place p;
   Unit w{};
-  Cut cut{};
-  if (c_attn_spins == 0) {
-    if (lane == 0) a.cuts[blockIdx.x] = cut;
-    return;
-  }
+  if (spins() == 0) return;
   Seq s;
   const bool any = find_place(a, blockIdx.x, gridDim.x, line, p, s);
   if (!any) {
     if (lane == 0) {
-      a.cuts[blockIdx.x] = cut;
       w.flags = kNone | kLast;
       x->unit[0] = w;
     }
@@ -348,7 +349,8 @@ __device__ void scheduler(const AttnArgs& a, const CUtensorMap* qm, uint8_t* q_s
     if (!wait(&x->u_empty[u & 1], ((u >> 1) & 1) ^ 1, x, handed)) break;
     if (lane == 0) x->unit[u & 1] = w;
     arrive_warp(&x->u_full[u & 1]);
-    if (w.t0 == 0 && w.n > 0 && w.n < all) {  // the unit's first piece: its cut
+    if (w.t0 == 0 && w.n > 0 && w.n < all && lane == 0) {  // the unit's first piece: its cut
+      Cut& cut = x->cut;
       cut.pieces = 1 + (int)div64(all - w.n + line.per - 1, line.per);
       cut.start = w.start, cut.hk = w.hk, cut.f0 = w.f0, cut.rows = w.rows;
       cut.first = u == 0 ? 0 : 1;
@@ -402,7 +404,6 @@ __device__ void scheduler(const AttnArgs& a, const CUtensorMap* qm, uint8_t* q_s
       }
     }
   }
-  if (lane == 0) a.cuts[blockIdx.x] = cut;
   if (*(volatile int*)&x->abort)  // after a wait that gave up, copies in flight land before the block ends
     for (uint32_t u = loads > 2 ? loads - 2 : 0; u < loads; ++u)
       mbar_wait_bounded(&x->q_full[u & 1], (u >> 1) & 1, kSpins);
@@ -854,7 +855,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   Aux* x = reinterpret_cast<Aux*>(ring + kRing * kBuf);
   const int warp = threadIdx.x >> 5;
   if (smem_u32(q_sm) & 1023) {  // swizzled tiles need it; dynamic shared memory starts there
-    if (threadIdx.x == 0) atomicExch(&g_attn_status, CAS_ERR_CUDA);
+    if (threadIdx.x == 0) {
+      atomicExch(&g_attn_status, CAS_ERR_CUDA);
+      a.cuts[blockIdx.x] = Cut{};
+    }
     return;
   }
   if (threadIdx.x == 0) {
@@ -877,6 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&x->spoilt, 8);
     mbar_init(&x->drain, 1);
     x->abort = x->any_bad[0] = x->any_bad[1] = 0;
+    x->cut = Cut{};
     fence_mbar_init();
     fence_async_smem();
   }
@@ -909,6 +914,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 0) tm_free(x->tmem, 512);
+  if (threadIdx.x == 0) {
+    x->cut.ok = !x->abort;
+    a.cuts[blockIdx.x] = x->cut;
+  }
 }
 constexpr size_t kSmem = (2 + kRing) * (size_t)kBuf + sizeof(Aux);
 static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -939,7 +948,11 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
   pdl_wait();
   pdl_trigger();
   const Cut cut = a.cuts[blockIdx.x];
+  const int ctas = gridDim.x + 1 - blockIdx.x;  // from the cut's on
+  bool ok = threadIdx.x >= ctas || a.cuts[blockIdx.x + threadIdx.x].ok || threadIdx.x >= cut.pieces;
   if (cut.pieces < 2) return;
+  for (int k = threadIdx.x + kJoinThreads; k < cut.pieces; k += kJoinThreads) ok = ok && a.cuts[blockIdx.x + k].ok;
+  if (!__syncthreads_and(ok)) return;  // a CTA gave up: what lies at its pieces' places is not this call's
   const int chunks = 32 / gridDim.y, items = cut.rows * chunks;
   int width = 4;  // threads side by side on items: a power of two
   while (width < items && width < kJoinThreads) width *= 2;
@@ -1038,8 +1051,8 @@ int attn_wait_status(bool clear) {
   return s;
 }
 
-int set_attn_spins(uint32_t spins) {
-  return cudaMemcpyToSymbol(c_attn_spins, &spins, sizeof(spins)) == cudaSuccess ? CAS_OK : CAS_ERR_CUDA;
+int set_attn_spins(uint32_t n) {
+  return cudaMemcpyToSymbol(c_attn_spins, &n, sizeof(n)) == cudaSuccess ? CAS_OK : CAS_ERR_CUDA;
 }
 
 }  // namespace cas

@@ -122,7 +122,9 @@ int cas_device_status(void* stream);
  * first wait for later launches: 0 makes it give up at once, 0xFFFFFFFF
  * restores the normal limit. With 0, cas_paged_attn's warps also wait for work
  * that is never handed out, give up, record CAS_ERR_TIMEOUT and write no
- * output. Synchronises the device; returns CAS_OK or CAS_ERR_CUDA. */
+ * output; with 1, those of every second CTA do, and rows that need such a CTA's
+ * part stay as they were. Synchronises the device; returns CAS_OK or
+ * CAS_ERR_CUDA. */
 int cas_test_first_wait_spins(uint32_t spins);
 /* Launch overlap, process-wide, off by default. When on, the kernels of later
  * calls are launched with programmatic stream serialization: a kernel's

@@ -557,6 +557,32 @@ def test_paged_attn_wait_that_runs_out_is_reported(cas):
     assert cas.cas_device_status() == 0
 
 
+def test_paged_attn_pieces_of_a_cta_that_gave_up_are_not_joined(cas):
+    """Every second CTA gives up: rows are right or as they were, whatever an
+    earlier call has left in the workspace."""
+    chunks, lens = [1, 40] + [1] * 200 + [3, 90], [9000, 3000] + [50 + i for i in range(200)] + [12000, 2500]
+    starts, lens, table, n_pages, rows = batch(chunks, lens, 32, seed=2)
+    k, v = pools(n_pages, 32, 2, "tokens", seed=2)
+    args = dev32(starts, lens, table)
+    q = torch.randn(rows, 8, D, device="cuda").to(BF)
+    ws = torch.empty(cas.cas_paged_attn_workspace_bytes(rows, 8, 2), dtype=torch.uint8, device="cuda")
+    want = cas.paged_attn(q, k, v, *args).view(BF)
+    cas.paged_attn(-q, k, v, *args, workspace=ws)
+    out = torch.full((rows, 8, D), 5.0, dtype=BF, device="cuda")
+    try:
+        assert cas.lib().cas_test_first_wait_spins(1) == 0
+        cas.paged_attn(q, k, v, *args, out=out, workspace=ws)
+        assert cas.cas_device_status() == -8
+    finally:
+        assert cas.lib().cas_test_first_wait_spins(0xFFFFFFFF) == 0
+    right, old = (out == want).all(-1), (out == 5).all(-1)
+    assert (right | old).all() and right.any() and old.any()
+    assert old[0].all() and old[-90:].all()  # cut into pieces of several CTAs
+    cas.paged_attn(q, k, v, *args, out=out, workspace=ws)
+    assert torch.equal(out, want)
+    assert cas.cas_device_status() == 0
+
+
 def test_misplaced_tensors_are_refused(cas):
     k, v = pools(4, 16, 2, "tokens")
     args = dev32([0, 2], [5], [[0, 1]])
