@@ -52,8 +52,15 @@
 // such a CTA holds a piece of are not joined.
 //
 // Rounding: scores, statistics and sums are fp32; P is rounded to bf16 for the
-// product with V (2^-8 relative each, the size of the output's own rounding),
-// the sum takes it unrounded. Measured on units that one CTA takes whole (as
+// product with V, the sum takes it unrounded. In calls of at most 128 rows of a
+// kv head a sequence on average (LOW: decoding, drafted tokens) units of at most
+// 128 rows multiply V by what that rounding left as well, a second product with
+// P good to 2^-17 as in the compressed cache's attention; the output's distance
+// from 64 bits is then that of its own rounding (0.168 % instead of 0.24 %). That
+// costs one token over 32K 41 instead of 38 us, 61 ragged ones 175 instead of
+// 168; for units of 256 rows it would be 983 instead of 702 us (2048 rows over
+// 32K), and the unused code alone 105 instead of 93 us for five ragged prompts
+// (first fetch of the instructions), so prompts have a kernel without it. Measured on units that one CTA takes whole (as
 // if the tensor cores cut their sums instead of rounding them), the output is 0.05 % small at 128K tokens, 0.33 % at
 // 1M, 1.5 % at 4M; spread over the GPU, one token over 4M shows nothing of it.
 #include <cuda.h>
@@ -74,6 +81,7 @@ constexpr int kUnit = 2 * kTile;           // flat rows a unit
 constexpr int kRing = 5;                   // K / V buffers: with two Q tiles all of the shared memory
 constexpr uint32_t kBuf = kTile * 256;     // bytes of a K or V tile
 constexpr uint32_t kHalf = kBuf / 2;       // 64 of the 128 dimensions
+constexpr int kLowPart = kTile / 2;        // columns of S behind P
 constexpr int kThreads = 384;               // three warpgroups of 168 registers a thread at launch
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;  // 2 * 216 + 72 = 3 * 168: the softmax keeps a row of S
 constexpr int kUnitCells = 2;              // cells of the line for a change of units: about two tiles' time
@@ -461,6 +469,7 @@ __device__ void producer(const AttnArgs& a, const CUtensorMap* map, uint8_t* rin
 // A step of a slot is P V of one tile and the scores of the next: one elected
 // lane issues both and their signals without a wait in between, since the K and
 // V tiles that it needs are waited for before P is (they are there long since).
+template <bool LOW>
 __device__ void issuer(uint32_t q_sm, uint32_t ring_sm, Aux* x) {
   const uint32_t tm = __reduce_max_sync(CAS_FULL, x->tmem);
   constexpr uint32_t id_s = tc_idesc_bf16(kTile, kTile, false), id_o = tc_idesc_bf16(kTile, CAS_BLK, true);
@@ -476,9 +485,10 @@ __device__ void issuer(uint32_t q_sm, uint32_t ring_sm, Aux* x) {
     tc_product_ss(tm + slot * kTile, tc_desc_lo(q_sm + tile * kBuf, 16), tc_desc_lo(ring_sm + k.slot * kBuf, 16), id_s);
     tc_commit(&x->s_full[slot]);
   };
-  auto values = [&](int slot, const Turn& v, bool add) {
-    tc_product_ts(tm + 2 * kTile + slot * CAS_BLK, tm + slot * kTile, tc_desc_lo(ring_sm + v.slot * kBuf, kHalf), id_o,
-                  add);
+  auto values = [&](int slot, const Turn& v, bool add, bool low) {
+    const uint32_t o = tm + 2 * kTile + slot * CAS_BLK, p = tm + slot * kTile, b = tc_desc_lo(ring_sm + v.slot * kBuf, kHalf);
+    tc_product_ts(o, p, b, id_o, add);
+    if (low) tc_product_ts(o, p + kLowPart, b, id_o, 1);
   };
   auto release = [&](const Turn& t) { tc_commit(&x->kv_empty[t.slot]); };
   for (uint32_t u = 0; ok; ++u) {
@@ -503,7 +513,7 @@ __device__ void issuer(uint32_t q_sm, uint32_t ring_sm, Aux* x) {
         if (more) arrived(kt);
         wait_p(0);
         if (ok && elect_one()) {
-          values(0, vt, j > 0);
+          values(0, vt, j > 0, false);
           if (more) {
             scores(0, 0, kt);
             if (last) tc_commit(&x->q_empty[0]);
@@ -514,7 +524,7 @@ __device__ void issuer(uint32_t q_sm, uint32_t ring_sm, Aux* x) {
         __syncwarp();
         wait_p(1);
         if (ok && elect_one()) {
-          values(1, vt, j > 0);
+          values(1, vt, j > 0, false);
           release(vt);
           if (more) {
             scores(1, 1, kt);
@@ -548,7 +558,7 @@ __device__ void issuer(uint32_t q_sm, uint32_t ring_sm, Aux* x) {
         arrived(vt);
         wait_p(i);
         if (ok && elect_one()) {
-          values(i, vt, j >= 2);
+          values(i, vt, j >= 2, LOW);
           release(vt);
           if (!more) tc_commit(&x->o_full[i]);
         }
@@ -640,6 +650,34 @@ __device__ bool guard_values(const Unit& w, uint32_t u, int slot, int key0, uint
   return true;
 }
 
+// P = 2^(s kScaleLog2 - ref) of a row's 128 scores as bf16 into its columns at
+// tm_s, with LOW what the rounding left of it behind; returns the sum of P.
+template <bool LOW>
+__device__ __forceinline__ float weigh_keys(const uint32_t s[kTile], float ref, uint32_t tm_s) {
+  const uint64_t sc2 = pack2(kScaleLog2, kScaleLog2), ref2 = pack2(-ref, -ref);
+  uint64_t ls[2] = {0, 0};
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t p[32], q[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      float e0, e1;
+      unpack2(fma2(pack2(__uint_as_float(s[64 * c + 2 * k]), __uint_as_float(s[64 * c + 2 * k + 1])), sc2, ref2), e0, e1);
+      e0 = ex2(e0);
+      e1 = ex2(e1);
+      ls[k & 1] = add2(ls[k & 1], pack2(e0, e1));
+      p[k] = pack_bf16x2(e0, e1);
+      if (LOW) q[k] = pack_bf16x2(e0 - __uint_as_float(p[k] << 16), e1 - __uint_as_float(p[k] & 0xFFFF0000u));
+    }
+    tm_st32(tm_s + 32 * c, p);
+    if (LOW) tm_st32(tm_s + kLowPart + 32 * c, q);
+  }
+  float l0, l1;
+  unpack2(add2(ls[0], ls[1]), l0, l1);
+  return l0 + l1;
+}
+
+template <bool LOW>
 __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
   const int slot = (threadIdx.x >> 7) - 1, r = threadIdx.x & 127, warp = r >> 5;
   const uint32_t tm = x->tmem + ((uint32_t)warp << 21);
@@ -719,26 +757,7 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        const uint64_t sc2 = pack2(kScaleLog2, kScaleLog2), ref2 = pack2(-ref, -ref);
-        uint64_t ls[2] = {0, 0};
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t p[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            float e0, e1;
-            unpack2(fma2(pack2(__uint_as_float(s[64 * c + 2 * k]), __uint_as_float(s[64 * c + 2 * k + 1])), sc2, ref2), e0,
-                    e1);
-            e0 = ex2(e0);
-            e1 = ex2(e1);
-            ls[k & 1] = add2(ls[k & 1], pack2(e0, e1));
-            p[k] = pack_bf16x2(e0, e1);
-          }
-          tm_st32(tm_s + 32 * c, p);
-        }
-        float l0, l1;
-        unpack2(add2(ls[0], ls[1]), l0, l1);
-        l += l0 + l1;
+        l += !LOW || two ? weigh_keys<false>(s, ref, tm_s) : weigh_keys<true>(s, ref, tm_s);
         tm_wait_st();
       }
       ++done;
@@ -847,6 +866,7 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
   }
 }
 
+template <bool LOW>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap km,
                       const __grid_constant__ CUtensorMap vm, const __grid_constant__ CUtensorMap qm) {
@@ -897,7 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    softmax(a, ring, x);
+    softmax<LOW>(a, ring, x);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == 1)
@@ -905,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (warp == 2)
       producer<true>(a, &vm, ring, x);
     else if (warp == 0)
-      issuer(smem_u32(q_sm), smem_u32(ring), x);
+      issuer<LOW>(smem_u32(q_sm), smem_u32(ring), x);
     else
       scheduler(a, &qm, q_sm, x);
   }
@@ -1093,10 +1113,13 @@ extern "C" int cas_paged_attn(const cas_paged_kv* kv, const cas_paged_batch* b, 
   CUtensorMap km, vm, qm{};
   if (!make_map(&km, kv, kv->k) || !make_map(&vm, kv, kv->v) || (a.q_box && !make_q_map(&qm, q, b->rows, n_q_heads, a.G)))
     return CAS_ERR_CUDA;
-  if (cudaFuncSetAttribute(paged_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
+  // few rows a sequence on average: bound by the traffic
+  const bool low = (int64_t)b->rows * a.G <= (int64_t)kTile * b->batch;
+  const auto kernel = low ? paged_attn_kernel<true> : paged_attn_kernel<false>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
     return CAS_ERR_CUDA;
   const cudaStream_t st = (cudaStream_t)stream;
-  if (const int e = launch_k(paged_attn_kernel, grid, kThreads, kSmem, st, a, km, vm, qm)) return e;
+  if (const int e = launch_k(kernel, grid, kThreads, kSmem, st, a, km, vm, qm)) return e;
   if (grid < 2) return CAS_OK;
   // directly behind our own kernel: its launch may overlap that kernel's tail
   // (pieces of 256 rows: two items a thread; of few rows: all in flight together)

@@ -348,6 +348,26 @@ def test_paged_attn_long_context_large_scores(cas):
     check_attn(cas, [2, 40], [20000, 9001], 8, 2, 64, scale=8.0)
 
 
+@pytest.mark.parametrize("chunks,lens,Hq,Hkv", [
+    ([1], [1], 8, 8), ([1, 1, 1], [700, 129, 5000], 32, 8), ([16], [2000], 32, 8), ([4, 7, 0, 32, 1], [900, 7, 0, 300, 64], 8, 2),
+    ([2], [6000], 64, 1),
+])
+def test_paged_attn_few_rows_keep_their_probabilities(cas, chunks, lens, Hq, Hkv):
+    """At most 128 rows of a kv head a sequence: probabilities in two bf16 terms,
+    as in the compressed cache's attention. Tolerance: 2^-16 of sum p |v| for what
+    two roundings leave (2^-17) and the sums' order, 2^-12 for scores whose fp32
+    error passes through the exponential, and the output's one rounding (the sum of
+    squares of which is at most that of 2^-9 / sqrt 3 of each value)."""
+    starts, lens, table, n_pages, rows = batch(chunks, lens, 32, seed=1)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v = pools(n_pages, 32, Hkv, "tokens", seed=1)
+    q = torch.randn(rows, Hq, D, generator=g, device="cuda").to(BF)
+    out = cas.paged_attn(q, k, v, *dev32(starts, lens, table)).view(BF)
+    ref, mass = serving.paged_attn(q, k, v, starts, lens, table)
+    err = (out.double() - ref).abs()
+    assert (err <= 2.0 ** -12 * mass + 2.0 ** -8 * ref.abs() + 1e-6).all()
+
+
 def test_paged_attn_long_units(cas):
     """Units of 32768 key tiles, two a CTA (every page of the table is the same
     one): no wait gives up, however long a unit takes.
