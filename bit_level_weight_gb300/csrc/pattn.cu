@@ -60,9 +60,13 @@
 // costs one token over 32K 41 instead of 38 us, 61 ragged ones 175 instead of
 // 168; for units of 256 rows it would be 983 instead of 702 us (2048 rows over
 // 32K), and the unused code alone 105 instead of 93 us for five ragged prompts
-// (first fetch of the instructions), so prompts have a kernel without it. Measured on units that one CTA takes whole (as
-// if the tensor cores cut their sums instead of rounding them), the output is 0.05 % small at 128K tokens, 0.33 % at
-// 1M, 1.5 % at 4M; spread over the GPU, one token over 4M shows nothing of it.
+// (first fetch of the instructions), so prompts have a kernel without it.
+//
+// The tensor cores cut the sums of their accumulators instead of rounding them
+// (as measured: the output of a unit that one CTA takes whole came out 0.05 %
+// small at 128K tokens, 0.33 % at 1M, 1.5 % at 4M), so a slot folds its O into
+// fp32 memory every kFold tiles: 0.011 % at every length from 128K to 4M, for 6 us
+// a fold (units of 1024 tiles each in a CTA: 1516 -> 1539 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -88,6 +92,7 @@ constexpr int kUnitCells = 2;              // cells of the line for a change of 
                                            // (1, 2, 3 of them: 104, 98, 98 us on five ragged prompts)
 constexpr int kMinCells = kUnitCells + 2;  // cells a CTA takes at least
 constexpr uint32_t kSpins = 1u << 20;        // polls of a wait
+constexpr int kFold = 256;                   // tiles that a slot's O adds up before it is folded away: a power of two
 constexpr int64_t kPieceFloats = kTile + 2;  // floats a row of a partial result: output, maximum, sum
 
 __device__ int g_attn_status = 0;
@@ -104,6 +109,7 @@ struct AttnArgs {
   uint16_t* o;
   struct Cut* cuts;  // [grid]: the unit that the cut behind CTA c is the first one in
   float* ws;         // [2 * grid] pieces of piece_rows rows: output [32][rows][4], maximum [rows], sum [rows]
+  float* ws1;        // [grid] pieces of min(piece_rows, 128) rows: what slot 1 folds of units of few rows
   int Hq, G, piece_rows;
   uint32_t gmul;     // f / G = (umulhi(f, gmul) + f) >> gshift for 0 <= f < 2^31
   int gshift;
@@ -513,7 +519,7 @@ __device__ void issuer(uint32_t q_sm, uint32_t ring_sm, Aux* x) {
         if (more) arrived(kt);
         wait_p(0);
         if (ok && elect_one()) {
-          values(0, vt, j > 0, false);
+          values(0, vt, j & (kFold - 1), false);
           if (more) {
             scores(0, 0, kt);
             if (last) tc_commit(&x->q_empty[0]);
@@ -524,7 +530,7 @@ __device__ void issuer(uint32_t q_sm, uint32_t ring_sm, Aux* x) {
         __syncwarp();
         wait_p(1);
         if (ok && elect_one()) {
-          values(1, vt, j > 0, false);
+          values(1, vt, j & (kFold - 1), false);
           release(vt);
           if (more) {
             scores(1, 1, kt);
@@ -558,7 +564,7 @@ __device__ void issuer(uint32_t q_sm, uint32_t ring_sm, Aux* x) {
         arrived(vt);
         wait_p(i);
         if (ok && elect_one()) {
-          values(i, vt, j >= 2, LOW);
+          values(i, vt, (j >> 1) & (kFold - 1), LOW);
           release(vt);
           if (!more) tc_commit(&x->o_full[i]);
         }
@@ -677,6 +683,47 @@ __device__ __forceinline__ float weigh_keys(const uint32_t s[kTile], float ref, 
   return l0 + l1;
 }
 
+// The tensor cores cut their sums, so a slot's O takes kFold tiles at most: then
+// it is added, relative to the maximum m of now, to what the row's place in the
+// workspace holds (`more`), and starts anew; at the unit's end (`back`) the sum
+// of both goes to tensor memory. Warp-wide; a thread reads what it wrote itself.
+__device__ __noinline__ void fold(const AttnArgs& a, bool own, bool first, int fr, bool mine, uint32_t tm_o, float m,
+                                  bool more, bool back) {
+  const int rows = own ? a.piece_rows : min(a.piece_rows, kTile);
+  float* place = own ? a.ws + (int64_t)(2 * blockIdx.x + (first ? 0 : 1)) * rows * kPieceFloats
+                     : a.ws1 + (int64_t)blockIdx.x * rows * kPieceFloats;
+  float* top = place + (int64_t)CAS_BLK * rows + fr;
+  const float fac = more && mine && m != -INFINITY ? ex2(*top - m) : 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t v[32];
+    tm_ld32(v, tm_o + 32 * c);
+    tm_wait_ld(v);
+    float4* at = reinterpret_cast<float4*>(place) + (int64_t)8 * c * rows + fr;
+    if (more && mine) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float4 t = at[(int64_t)k * rows];
+        const float old[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * k + i] = __float_as_uint(fmaf(old[i], fac, __uint_as_float(v[4 * k + i])));
+      }
+    }
+    if (back) {
+      tm_st32(tm_o + 32 * c, v);
+    } else if (mine) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        at[(int64_t)k * rows] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
+                                            __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
+    }
+  }
+  if (back)
+    tm_wait_st();
+  else if (mine)
+    *top = m;
+}
+
 template <bool LOW>
 __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
   const int slot = (threadIdx.x >> 7) - 1, r = threadIdx.x & 127, warp = r >> 5;
@@ -694,79 +741,96 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
     const int f = w.f0 + (mine ? fr : w.rows - 1), tok = div_g(a, f);
     const int lim = max(0, min(w.kv_end, w.pos0 + tok + 1)) - 1;
     const bool busy = __any_sync(CAS_FULL, mine);
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, l_fold = 0.f;
     int done = 0;
+    auto folds = [&](bool more, bool back) {
+      fold(a, two || slot == 0, w.flags & kFirst, fr, mine, tm_o, m, more, back);
+      l_fold += l;
+      l = 0.f;
+    };
     const int step = two ? 1 : 2;
-    for (int j = two ? 0 : slot; j < w.n; j += step) {
-      const int key0 = (w.t0 + j) * kTile;
-      if ((slot == 0 || !two) && (key0 + kTile > w.kv_end || guards(w, key0))) {
-        if (!guard_values(w, u, slot, key0, 2 * (base + j) + 1, ring, x)) return;
+    for (int j = two ? 0 : slot; j < w.n;) {
+      if (__builtin_expect(done > 0, 0)) {  // (the product before a tile's S is complete when S is)
+        if (!wait(&x->s_full[slot], ns & 1, x)) return;
+        tc_fence_after();
+        if (busy) folds(done > kFold, false);
       }
-      if (!wait(&x->s_full[slot], ns++ & 1, x)) return;
-      tc_fence_after();
-      if (busy) {
-        uint32_t s[kTile];
-        tm_ld32(s, tm_s);
-        tm_ld32(s + 32, tm_s + 32);
-        tm_wait_ld(s);
-        tm_wait_ld(s + 32);
-        tm_ld32(s + 64, tm_s + 64);
-        tm_ld32(s + 96, tm_s + 96);
-        const bool edge = __any_sync(CAS_FULL, key0 + kTile - 1 > lim);
-        const int last = lim - key0;
-        if (edge) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (c > last) s[c] = 0xFF800000u;
+      for (const int end = min(w.n, j + kFold * step); j < end; j += step) {
+        const int key0 = (w.t0 + j) * kTile;
+        if ((slot == 0 || !two) && (key0 + kTile > w.kv_end || guards(w, key0))) {
+          if (!guard_values(w, u, slot, key0, 2 * (base + j) + 1, ring, x)) return;
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (!wait(&x->s_full[slot], ns++ & 1, x)) return;
+        tc_fence_after();
+        if (busy) {
+          uint32_t s[kTile];
+          tm_ld32(s, tm_s);
+          tm_ld32(s + 32, tm_s + 32);
+          tm_wait_ld(s);
+          tm_wait_ld(s + 32);
+          tm_ld32(s + 64, tm_s + 64);
+          tm_ld32(s + 96, tm_s + 96);
+          const bool edge = __any_sync(CAS_FULL, key0 + kTile - 1 > lim);
+          const int last = lim - key0;
+          if (edge) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mx[k] = max3(mx[k], __uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1]));
-        tm_wait_ld(s + 64);
-        tm_wait_ld(s + 96);
-        if (edge) {
-#pragma unroll
-          for (int c = 64; c < kTile; ++c)
-            if (c > last) s[c] = 0xFF800000u;
-        }
-#pragma unroll
-        for (int c = 64; c < kTile; c += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mx[k] = max3(mx[k], __uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1]));
-        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * kScaleLog2;
-        const bool grow = mine && top > m + 8.f;
-        if (done == 0) {
-          m = top;
-        } else if (__any_sync(CAS_FULL, grow)) {
-          // rescale O: the product before this tile's S is complete when S is
-          const float fac = grow ? ex2(m - top) : 1.f;
-          if (grow) m = top;
-          l *= fac;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tm_ld32(v, tm_o + 32 * c);
-            tm_wait_ld(v);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * fac);
-            tm_st32(tm_o + 32 * c, v);
+            for (int c = 0; c < 64; ++c)
+              if (c > last) s[c] = 0xFF800000u;
           }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 64; c += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mx[k] = max3(mx[k], __uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1]));
+          tm_wait_ld(s + 64);
+          tm_wait_ld(s + 96);
+          if (edge) {
+#pragma unroll
+            for (int c = 64; c < kTile; ++c)
+              if (c > last) s[c] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int c = 64; c < kTile; c += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mx[k] = max3(mx[k], __uint_as_float(s[c + 2 * k]), __uint_as_float(s[c + 2 * k + 1]));
+          const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * kScaleLog2;
+          const bool grow = mine && top > m + 8.f;
+          if (done == 0) {
+            m = top;
+          } else if (__any_sync(CAS_FULL, grow)) {
+            // rescale O
+            const float fac = grow ? ex2(m - top) : 1.f;
+            if (grow) m = top;
+            l *= fac;
+            l_fold *= fac;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t v[32];
+              tm_ld32(v, tm_o + 32 * c);
+              tm_wait_ld(v);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * fac);
+              tm_st32(tm_o + 32 * c, v);
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          // (what is expected lies in the loop: one token over 32K 40.8 us, 41.8 the other way round)
+          if (LOW && __builtin_expect(!two, 1))
+            l += weigh_keys<true>(s, ref, tm_s);
+          else
+            l += weigh_keys<false>(s, ref, tm_s);
+          tm_wait_st();
         }
-        const float ref = m == -INFINITY ? 0.f : m;
-        l += !LOW || two ? weigh_keys<false>(s, ref, tm_s) : weigh_keys<true>(s, ref, tm_s);
-        tm_wait_st();
+        ++done;
+        tc_fence_before();
+        if (pending) {
+          if (!wait(&x->merged, (nm - 1) & 1, x)) return;
+          pending = false;
+        }
+        arrive_warp(&x->p_full[slot]);
       }
-      ++done;
-      tc_fence_before();
-      if (pending) {
-        if (!wait(&x->merged, (nm - 1) & 1, x)) return;
-        pending = false;
-      }
-      arrive_warp(&x->p_full[slot]);
     }
     base += w.n;
     // ---- epilogue
@@ -777,6 +841,10 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
     if (done > 0) {
       if (!wait(&x->o_full[slot], no++ & 1, x)) return;
       tc_fence_after();
+      if (__builtin_expect(busy && done > kFold, 0)) {
+        folds(true, true);
+        l = l_fold;
+      }
     }
     float w0 = 1.f, w1 = 0.f;  // weights of the two slots' outputs
     int c0 = 0, c1 = 4;        // 32-column chunks that this thread writes
@@ -1081,8 +1149,8 @@ using namespace cas;
 
 extern "C" uint64_t cas_paged_attn_workspace_bytes(int rows, int n_q_heads, int n_kv_heads) {
   if (rows < 1 || n_q_heads < 1 || n_kv_heads < 1) return 16;
-  const int64_t g = sm_count();
-  return ((uint64_t)g * sizeof(Cut) + 255) / 256 * 256 + 2 * g * piece_rows(rows, n_q_heads, n_kv_heads) * kPieceFloats * 4;
+  const int64_t g = sm_count(), r = piece_rows(rows, n_q_heads, n_kv_heads);
+  return ((uint64_t)g * sizeof(Cut) + 255) / 256 * 256 + g * (2 * r + std::min<int64_t>(r, kTile)) * kPieceFloats * 4;
 }
 
 extern "C" int cas_paged_attn(const cas_paged_kv* kv, const cas_paged_batch* b, const uint16_t* q, int n_q_heads,
@@ -1107,6 +1175,7 @@ extern "C" int cas_paged_attn(const cas_paged_kv* kv, const cas_paged_batch* b, 
   a.wide = ((uintptr_t)o & 31) == 0;
   a.G = n_q_heads / kv->n_kv_heads;
   a.piece_rows = piece_rows(b->rows, n_q_heads, kv->n_kv_heads);
+  a.ws1 = a.ws + (int64_t)2 * grid * a.piece_rows * kPieceFloats;
   while ((1 << a.gshift) < a.G) ++a.gshift;
   a.gmul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << a.gshift) - a.G)) / a.G + 1);
   a.q_box = kTile % a.G == 0;

@@ -573,10 +573,8 @@ int cas_paged_append(const cas_paged_kv* kv, const cas_paged_batch* b, const voi
  * scores, statistics and sums, probabilities rounded to bf16 for the tensor
  * cores; where rows * n_q_heads / n_kv_heads <= 128 * batch (decoding, drafted
  * tokens), sequences of at most 128 such rows take them in two bf16 terms, good
- * to 2^-17. Over long contexts the tensor cores' fp32 sums come out small,
- * in long chunks of rows by about 4e-9 of the output's magnitude a token of
- * context (measured 0.05 % at 128K, 0.33 % at 1M; bf16 rounds by up to 0.39 %). A row
- * that sees no key is zero. Keys and values at positions that a
+ * to 2^-17. No sum's error grows with the context (the tensor cores cut theirs:
+ * they add up 256 tiles of 128 keys at most). A row that sees no key is zero. Keys and values at positions that a
  * row does not see never reach it, whatever they hold; one that it sees and
  * that is not finite makes its output not finite (of a value: in that
  * dimension). Calls that may overlap on the GPU need a workspace each. The

@@ -354,10 +354,9 @@ def test_paged_attn_long_context_large_scores(cas):
 ])
 def test_paged_attn_few_rows_keep_their_probabilities(cas, chunks, lens, Hq, Hkv):
     """At most 128 rows of a kv head a sequence: probabilities in two bf16 terms,
-    as in the compressed cache's attention. Tolerance: 2^-16 of sum p |v| for what
-    two roundings leave (2^-17) and the sums' order, 2^-12 for scores whose fp32
-    error passes through the exponential, and the output's one rounding (the sum of
-    squares of which is at most that of 2^-9 / sqrt 3 of each value)."""
+    as in the compressed cache's attention. Tolerance: the output's one rounding,
+    and 2^-12 of sum p |v| for the scores' fp32 error and all that is smaller (the
+    two terms 2^-17, the exponentials 2^-21)."""
     starts, lens, table, n_pages, rows = batch(chunks, lens, 32, seed=1)
     g = torch.Generator(device="cuda").manual_seed(1)
     k, v = pools(n_pages, 32, Hkv, "tokens", seed=1)
@@ -395,6 +394,37 @@ def test_paged_attn_long_units(cas):
     tol = (2.0 ** -8 + 2.0 ** -12 + 2.0 ** 18 * 2.0 ** -23) * mass + (2.0 ** -8 + 2.0 ** 15 * 2.0 ** -23) * ref.abs()
     print("worst", (err / mass).max().item())
     assert (err <= tol).all(), f"worst {(err / tol).max().item():.3g}"
+
+
+@pytest.mark.parametrize("B,T,G,n", [(1, 9728, 4, 1 << 17), (1, 9728, 4, 1 << 20), (1, 9728, 4, 1 << 22),
+                                     (200, 1, 1, 1 << 20), (170, 7, 4, 1 << 19), (40, 200, 1, 1 << 20)])
+def test_paged_attn_sums_do_not_shrink_with_the_context(cas, B, T, G, n):
+    """Units of up to 32768 key tiles, one page throughout: the tensor cores' sums
+    must not lose what grows with the number of tiles.
+
+    A slot's O takes at most 256 tiles of 8 products (few rows: 16, of two terms of
+    P) in a row, 2^12 additions, each of which cuts at most 2^-23 of the sum; the
+    rest is rounded to nearest. So the outputs' mean is off by 2^-11 of sum p |v|
+    at most, and by the mean of 3840 or more roundings (of 2^-9 each in the root
+    mean square: 2^-15 together, taken four times). Each output as elsewhere."""
+    page = 1024
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k = torch.randn(1, page, 1, D, generator=g, device="cuda").to(BF)
+    v = (1 + torch.randn(1, page, 1, D, generator=g, device="cuda")).to(BF)
+    q = torch.randn(B * T, G, D, generator=g, device="cuda").to(BF)
+    out = cas.paged_attn(q, k, v, *dev32([T * b for b in range(B + 1)], [n] * B), torch.zeros(B, n // page, dtype=torch.int32,
+                                                                                        device="cuda")).view(BF)
+    assert cas.cas_device_status() == 0
+    pick = torch.unique(torch.tensor([0, 1, T // 2, T - 2, T - 1, (B // 2) * T, B * T - 1, (B - 3) * T + T // 3,
+                                      *range(0, B * T, max(1, B * T // 30))], device="cuda").clamp(0, B * T - 1))
+    count = (n - T + pick % T)[:, None] - torch.arange(page, device="cuda")
+    s = q[pick].double() @ k[0, :, 0].double().T / D ** 0.5
+    w = torch.softmax(s + (count // page + 1)[:, None, :].double().log(), -1)
+    ref, mass = w @ v[0, :, 0].double(), w @ v[0, :, 0].double().abs()
+    err = out[pick].double() - ref
+    print("mean", (err.sum() / mass.sum()).item())
+    assert (err.abs() <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -12) * mass + 2.0 ** -8 * ref.abs()).all()
+    assert err.sum().abs() <= (2.0 ** -11 + 2.0 ** -13) * mass.sum()
 
 
 def test_paged_attn_offsets_beyond_32_bits(cas):
