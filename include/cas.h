@@ -575,9 +575,10 @@ int cas_paged_append(const cas_paged_kv* kv, const cas_paged_batch* b, const voi
  * tokens), sequences of at most 128 such rows take them in two bf16 terms, good
  * to 2^-17. No sum's error grows with the context (the tensor cores cut theirs:
  * they add up 256 tiles of 128 keys at most). A row that sees no key is zero. Keys and values at positions that a
- * row does not see never reach it, whatever they hold; one that it sees and
- * that is not finite makes its output not finite (of a value: in that
- * dimension). Calls that may overlap on the GPU need a workspace each. The
+ * row does not see never reach it, whatever they hold. A value that it sees and
+ * that is not finite makes that dimension of its output not finite. A score of
+ * NaN or +inf makes the row not finite, one of -inf (an infinite key or query)
+ * weighs nothing, and a row whose scores are all -inf is zero. Calls that may overlap on the GPU need a workspace each. The
  * same call gives the same bits. Errors: CAS_ERR_INVALID for the
  * descriptors as in cas_paged_append, n_q_heads not a multiple of n_kv_heads
  * or a null or misaligned q or o; CAS_ERR_BUFFER if the workspace is null, not

@@ -314,6 +314,32 @@ def test_paged_attn_many_units_a_cta(cas, chunks, deep):
     assert cas.cas_device_status() == 0
 
 
+@pytest.mark.parametrize("T,n", [(1, 1), (1, 300), (3, 9000), (90, 700)])
+def test_paged_attn_infinite_scores(cas, T, n):
+    """Keys of which one (all: n = 1) holds an infinity or NaN: a score of +inf or
+    NaN spoils the row, one of -inf weighs nothing, nothing but -inf gives zeros."""
+    page, Hq, Hkv = 32, 8, 2
+    starts, lens, table, n_pages, rows = batch([T], [n], page, seed=8)
+    k, v = pools(n_pages, page, Hkv, "tokens", seed=8)
+    q = torch.randn(rows, Hq, D, generator=torch.Generator(device="cuda").manual_seed(8), device="cuda").to(BF)
+    q[:, ::2, 5], q[:, 1::2, 5] = 1.0, -1.0
+    at = (n - T) // 2  # every row sees it
+    where = table[0][at // page], at % page, slice(None), 5
+    for x in (float("inf"), float("-inf"), float("nan")):
+        k[where] = x
+        out = cas.paged_attn(q, k, v, *dev32(starts, lens, table)).view(BF)
+        low = torch.zeros(Hq, dtype=torch.bool, device="cuda")  # heads whose score there is -inf
+        if x == x:
+            low[(slice(1, None, 2) if x > 0 else slice(0, None, 2))] = True
+        assert not torch.isfinite(out[:, ~low]).any()
+        if n == 1:
+            assert (out[:, low] == 0).all()
+        elif x == x:
+            ref, mass = serving.paged_attn(q, k, v, starts, lens, table)
+            err = (out[:, low].double() - ref[:, low]).abs()
+            assert (err <= (2.0 ** -8 + 2.0 ** -12) * mass[:, low] + 2.0 ** -8 * ref[:, low].abs() + 1e-6).all()
+
+
 def test_paged_attn_rows_far_before_the_first_token(cas):
     """A length below the chunk's: the rows before position 0 see no key and are
     zero, also those more than 2^16 before values that are not finite."""
