@@ -13,9 +13,11 @@
 // a few rows, the launch (5-6 us).
 //
 // Angle: theta^(-i/64) / 2 pi is a fraction of a turn per position, held as a
-// 64-bit fixed-point number f_i (units of 2^-64 turns, good to 2^-53 of itself).
-// p * f_i modulo 2^64 is the angle reduced to a turn, and its top 32 bits go
-// to sincospif: no double precision sine per row, whose 64 evaluations would
+// 64-bit fixed-point number f_i in units of 2^-64 turns, the product of two
+// constants. p * f_i modulo 2^64 is the angle reduced to a turn. f_i is off by less
+// than 2^-55 turns (the constants' rounding: 2^-63 turns in A, a few 2^-53 of itself
+// in both), the angle by |p| times that: 2^-24 turns at |p| = 2^31. Its top 32 bits
+// go to sincospif: no double precision sine per row, whose 64 evaluations would
 // cost more than the row's traffic on a GPU with 2 fp64 lanes a SM and clock.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -460,8 +460,9 @@ enum {
  * (CAS_T_F32 or CAS_T_BF16), q heads then k heads then v heads. A q head x
  * becomes rot(x / sqrt(mean(x^2) + eps) * gamma_q), a k head the same with
  * gamma_k; gamma_q, gamma_k: bf16 [128], NULL for no norm. rot turns the pair
- * (i, i + 64) as in cas_rope_split by the angle p * theta^(-i/64), reduced
- * exactly modulo a turn in 64-bit fixed point; row r has position p = pos[r]
+ * (i, i + 64) as in cas_rope_split by the angle p * theta^(-i/64), formed and
+ * reduced modulo a turn in 64-bit fixed point (off by |p| * 2^-55 turns at most,
+ * 2^-24 at the last position; the reduction adds nothing); row r has position p = pos[r]
  * (int32 [rows], any value), or pos0 + r % rows_per_seq when pos is NULL. fp32
  * arithmetic; outputs bf16, rounded once: q [rows][n_q_heads][128]; k and v
  * rows of n_kv_heads * 128 values at strides k_row_stride / v_row_stride

@@ -66,6 +66,18 @@ def test_qk_norm_rope(cas, rows, Hq, Hkv, dtype, norm, positions):
     assert (np.abs(f64(v) - rv) <= 2.0 ** -8 * np.abs(rv)).all()
 
 
+@pytest.mark.parametrize("theta", [10.0, 1e4, 5e5, 1e7, 1e8])
+def test_qk_norm_rope_far_positions(cas, theta):
+    """Angles at positions of up to 31 bits: off by 2^-24 turns at most, which with
+    the 2^-21 for sine and cosine stays below 2^-18 of a pair's magnitude."""
+    p = np.array([0, 1, 2 ** 20 + 3, 2 ** 24 - 1, 2 ** 29 + 12345, 2 ** 30 + 1, 2 ** 31 - 1, -1, -77777, -2 ** 31], np.int32)
+    qkv = torch.randn(len(p), 6 * D, generator=torch.Generator().manual_seed(4))
+    q, k, _ = cas.qk_norm_rope(qkv.cuda(), 4, 1, pos=torch.from_numpy(p).cuda(), theta=theta)
+    rq, rk, _, qn, kn = serving.qk_norm_rope(qkv.double().numpy(), 4, 1, None, None, 1e-6, p, theta)
+    near_rotated(f64(q), rq, qn)
+    near_rotated(f64(k), rk, kn)
+
+
 def test_qk_norm_rope_into_wider_rows(cas):
     """k and v rows land in a larger buffer; what lies between stays."""
     rows, Hq, Hkv = 5, 4, 2
