@@ -818,8 +818,10 @@ def _paged(rows: int, k: torch.Tensor, v: torch.Tensor, row_start, kv_len, pages
     if k.dtype not in _BF16 or v.dtype not in _BF16 or k.dim() != 4 or k.shape[3] != 128 or v.shape != k.shape:
         raise ValueError("k_pages and v_pages: bf16 [n_pages][page_size][n_kv_heads][128] of one shape")
     n, size, heads, _ = k.shape
-    sp, st, sh, sd = k.stride()
-    if v.stride() != (sp, st, sh, sd) or sd != 1:
+    sp, st, sh, sd = ks = k.stride()
+    vs = v.stride()
+    # a stride over an extent of one is never used, and torch may report any
+    if sd != 1 or (vs != ks and any(a != b and e > 1 for a, b, e in zip(ks, vs, k.shape))):
         raise ValueError("k_pages and v_pages: equal strides with contiguous heads expected")
     batch = kv_len.shape[0] if kv_len.dim() == 1 else -1
     _is_i32(row_start, (batch + 1,), "row_start")
@@ -828,7 +830,6 @@ def _paged(rows: int, k: torch.Tensor, v: torch.Tensor, row_start, kv_len, pages
         raise ValueError("pages: int32 [batch][max_pages] expected")
     if k.get_device() != i or v.get_device() != i:
         raise ValueError(f"libcas takes device tensors of one device: got {k.device} and {v.device}")
-    # a stride over an extent of one is never used, and torch may report any
     kv = cas_paged_kv(heads, size, n, k.data_ptr(), v.data_ptr(), sp if n > 1 else 128, st if size > 1 else 128,
                       sh if heads > 1 else 128)
     return kv, cas_paged_batch(batch, rows, pages.shape[1], 0, _raw(row_start, i), _raw(kv_len, i), _raw(pages, i))

@@ -159,6 +159,16 @@ def test_paged_binding(kw, what):
         cas.paged_attn(z(2, 4, 128, dtype=BF), workspace=z(256, dtype=torch.uint8), **a)
 
 
+@pytest.mark.parametrize("n,heads", [(1, 2), (8, 1), (1, 1)])
+def test_paged_strides_over_one_do_not_matter(n, heads):
+    """One page or one head: torch's stride over it may be any, and differ between the pools."""
+    k = z(n, 16, heads, 128, dtype=BF)
+    v = k.as_strided(k.shape, [s if e > 1 else 7 * s + 1 for s, e in zip(k.stride(), k.shape)])
+    assert v.stride() != k.stride()
+    kv, _ = cas._paged(2, k, v, z(2), z(1), z(1, 3), -1)
+    assert (kv.page_stride, kv.token_stride, kv.head_stride) == (16 * heads * 128 if n > 1 else 128, heads * 128, 128)
+
+
 @pytest.mark.parametrize("kw,what", [
     (dict(x=z(2, 3, dtype=torch.int64)), "x"),
     (dict(u=None), "draft and u"),
