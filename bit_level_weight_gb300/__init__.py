@@ -869,7 +869,7 @@ def paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, ro
                kv_len: torch.Tensor, pages: torch.Tensor, out: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """q [rows][Hq][128] -> o bf16 bit patterns [rows][Hq][128] over the paged
-    cache: every row sees its sequence's positions up to its own."""
+    cache: every row sees its sequence's positions up to its own. out may be q."""
     if stream is not None:
         return _with_stream(stream, q, paged_attn, q, k_pages, v_pages, row_start, kv_len, pages, out, workspace)
     if q.dim() != 3:

@@ -1161,6 +1161,11 @@ extern "C" int cas_paged_attn(const cas_paged_kv* kv, const cas_paged_batch* b, 
   if (b->rows == 0 || b->batch == 0) return CAS_OK;
   if (!q || !o || !aligned16(q) || !aligned16(o)) return CAS_ERR_INVALID;
   if ((int64_t)b->rows * n_q_heads > 0x7FFFFFFF - kUnit) return CAS_ERR_INVALID;
+  // o may be q: a row is written when all CTAs that need its q are through with it, by the CTA that takes
+  // its unit whole or by the join, and what a Q tile holds of other units' rows is not used
+  const uint64_t n = (uint64_t)b->rows * n_q_heads * CAS_BLK * sizeof(uint16_t);
+  const uint64_t qa = (uint64_t)(uintptr_t)q, oa = (uint64_t)(uintptr_t)o;
+  if (qa != oa && qa < oa + n && oa < qa + n) return CAS_ERR_INVALID;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < cas_paged_attn_workspace_bytes(b->rows, n_q_heads, kv->n_kv_heads))
     return CAS_ERR_BUFFER;

@@ -466,8 +466,8 @@ enum {
  * (int32 [rows], any value), or pos0 + r % rows_per_seq when pos is NULL. fp32
  * arithmetic; outputs bf16, rounded once: q [rows][n_q_heads][128]; k and v
  * rows of n_kv_heads * 128 values at strides k_row_stride / v_row_stride
- * elements (multiples of 8, at least n_kv_heads * 128). A row never depends
- * on another. Errors: CAS_ERR_INVALID for rows < 0, head counts < 1 or above
+ * elements (multiples of 8, at least n_kv_heads * 128); no output overlaps an
+ * input or another output. A row never depends on another. Errors: CAS_ERR_INVALID for rows < 0, head counts < 1 or above
  * 4096, an unknown type, theta not above 1, a negative or NaN eps, pos0 < 0 or
  * rows_per_seq < 1 without pos, a null or misaligned pointer or a bad stride;
  * CAS_ERR_CUDA. rows = 0 does nothing. */
@@ -505,8 +505,8 @@ int cas_qk_norm_rope(const void* qkv, int qkv_type, int rows, int n_q_heads, int
  * token is -1. A drafted token outside 0..vocab-1 has ratio 0, a NaN u accepts
  * nothing, and u[b][gamma] outside [0, 1) takes the first or last token with
  * r > 0. The draw's sums are good to about 2^-35 and exact sums of its weights,
- * so the same call gives the same tokens; ratios are fp32. Calls that may overlap
- * on the GPU need a workspace each. Errors: CAS_ERR_INVALID for batch < 0 or above
+ * so the same call gives the same tokens; ratios are fp32. No output may overlap
+ * an input. Calls that may overlap on the GPU need a workspace each. Errors: CAS_ERR_INVALID for batch < 0 or above
  * 65535, gamma outside 0..64, vocab outside 1..2^31-1, a stride below vocab, a
  * temperature that is negative, NaN, infinite or positive but outside
  * [1e-6, 1e6], or a null pointer; CAS_ERR_BUFFER if the workspace is null,
@@ -558,7 +558,8 @@ typedef struct cas_paged_batch {
 /* Appends the rows' keys and values to the paged cache, with the norms and the
  * rotation of cas_qk_norm_rope on the way: qkv, gammas, eps and theta as
  * there; the position of a row is its token's. K and V heads go to the
- * token's slots, q to [rows][n_q_heads][128]. Two rows must not share a slot.
+ * token's slots, q to [rows][n_q_heads][128]. Two rows must not share a slot,
+ * and nothing written may overlap an input.
  * Errors: those of cas_qk_norm_rope; CAS_ERR_INVALID for a null descriptor
  * or pointer, a page size, stride or alignment out of range, batch < 0 or
  * max_pages < 1. rows = 0 or batch = 0 does nothing. */
@@ -581,8 +582,9 @@ int cas_paged_append(const cas_paged_kv* kv, const cas_paged_batch* b, const voi
  * NaN or +inf makes the row not finite, one of -inf (an infinite key or query)
  * weighs nothing, and a row whose scores are all -inf is zero. Calls that may overlap on the GPU need a workspace each. The
  * same call gives the same bits. Errors: CAS_ERR_INVALID for the
- * descriptors as in cas_paged_append, n_q_heads not a multiple of n_kv_heads
- * or a null or misaligned q or o; CAS_ERR_BUFFER if the workspace is null, not
+ * descriptors as in cas_paged_append, n_q_heads not a multiple of n_kv_heads,
+ * a null or misaligned q or o, or an o that overlaps q without being q (the
+ * same address is fine: the output then takes q's place); CAS_ERR_BUFFER if the workspace is null, not
  * 16-byte aligned or smaller than cas_paged_attn_workspace_bytes;
  * CAS_ERR_CUDA. rows = 0 or batch = 0 does nothing. */
 int cas_paged_attn(const cas_paged_kv* kv, const cas_paged_batch* b, const uint16_t* q, int n_q_heads, uint16_t* o,

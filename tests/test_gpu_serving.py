@@ -522,6 +522,21 @@ def test_paged_graph_follows_the_batch_on_the_device(cas):
         assert ((o.view(BF).double() - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("chunks,lens,Hq,Hkv", [([1], [9000], 32, 8), ([300, 1, 70, 600], [3000, 77, 70, 5000], 12, 4),
+                                                ([40, 64, 90] * 30, [700, 64, 90] * 30, 12, 2)])
+def test_paged_attn_in_place(cas, chunks, lens, Hq, Hkv):
+    """The output in q's own memory."""
+    starts, lens, table, n_pages, rows = batch(chunks, lens, 32, seed=4, pad_rows=2)
+    k, v = pools(n_pages, 32, Hkv, "tokens", seed=4)
+    args = dev32(starts, lens, table)
+    q = torch.randn(rows, Hq, D, device="cuda").to(BF)
+    want = cas.paged_attn(q, k, v, *args).view(BF)
+    for _ in range(5):
+        o = q.clone()
+        assert cas.paged_attn(o, k, v, *args, out=o) is o
+        assert torch.equal(o[:-2], want[:-2]) and torch.equal(o[-2:], q[-2:])
+
+
 def test_paged_attn_shared_and_repeated_pages(cas):
     """Two sequences share their first pages, and one holds a page twice."""
     k, v = pools(20, 32, 2, "tokens", seed=3)

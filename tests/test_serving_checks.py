@@ -80,6 +80,9 @@ def test_paged_calls_refuse(L):
                                   (GOOD, 4, GOOD, None, 1 << 40, -6), (GOOD, 4, GOOD, ODD, 1 << 40, -6),
                                   (GOOD, 4, GOOD, GOOD, 0, -6)):
         assert L.cas_paged_attn(kv, b, q, hq, o, ws, n, None) == want
+    # o over a part of q is refused (rows 2 x 4 heads x 256 bytes); q itself and what lies beside it pass on
+    for far, want in ((0, -6), (16, -1), (-16, -1), (2047 & ~15, -1), (-2032, -1), (2048, -6), (-2048, -6)):
+        assert L.cas_paged_attn(kv, b, GOOD, 4, GOOD + far, GOOD, 0, None) == want
 
 
 @pytest.mark.parametrize("none", [dict(rows=0), dict(batch=0)])
