@@ -31,13 +31,14 @@
 //                   ahead, with their Q rows
 //
 // What bounds it (measured on GB300, 8 kv heads, 32 query heads):
-//   one token a sequence: the K and V stream. 61 sequences of up to 8K: 166-171
-//     us for 1.0 GB = 5.8-6.0 TB/s, 86-88 % of the measured copy rate; one sequence of 32K:
-//     36-38 us for 134 MB, of which about 8 us are the way to the first tile (place
+//   one token a sequence: the K and V stream. 61 sequences of up to 8K: 172-177
+//     us for 1.0 GB = 5.7-5.8 TB/s, 83-86 % of the measured copy rate; one sequence of 32K:
+//     41 us for 134 MB, of which about 8 us are the way to the first tile (place
 //     on the line, page table, first TMA) and 4 us the join.
-//   long chunks: 2048 rows over 32K in 674-703 us = 1.52-1.58 PFLOP/s, about
-//     80 % of cuBLAS's burst rate on this GPU (738 us in long runs, where the power
-//     cap holds the SMs at 1890 MHz). A key tile takes 1.6 us where its four products
+//   long chunks: 2048 rows over 32K in 686-706 us = 1.51-1.55 PFLOP/s by themselves,
+//     78-80 % of cuBLAS's burst rate on this GPU; 750 us = 1.42 PFLOP/s in long runs,
+//     where the power cap holds the SMs at 1790 MHz, 73 % of the burst rate and 81 %
+//     of cuBLAS's sustained one. A key tile takes 1.6 us where its four products
 //     need 1.05: a slot's chain S -> softmax (0.7 us) -> P V, S is longer than what
 //     the other slot hides, and tensor memory holds no third slot (2 x (128 S +
 //     128 O) columns are all 512). Tried and slower: P V in two halves behind two
@@ -57,8 +58,8 @@
 // 128 rows multiply V by what that rounding left as well, a second product with
 // P good to 2^-17 as in the compressed cache's attention; the output's distance
 // from 64 bits is then that of its own rounding (0.168 % instead of 0.24 %). That
-// costs one token over 32K 41 instead of 38 us, 61 ragged ones 175 instead of
-// 168; for units of 256 rows it would be 983 instead of 702 us (2048 rows over
+// costs one token over 32K 41 instead of 38 us, 61 ragged ones 173 instead of
+// 167; for units of 256 rows it would be 983 instead of 702 us (2048 rows over
 // 32K), and the unused code alone 105 instead of 93 us for five ragged prompts
 // (first fetch of the instructions), so prompts have a kernel without it.
 //
