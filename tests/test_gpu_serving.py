@@ -435,7 +435,8 @@ def test_paged_attn_long_units(cas):
 
 
 @pytest.mark.parametrize("B,T,G,n", [(1, 9728, 4, 1 << 17), (1, 9728, 4, 1 << 20), (1, 9728, 4, 1 << 22),
-                                     (200, 1, 1, 1 << 20), (170, 7, 4, 1 << 19), (40, 200, 1, 1 << 20)])
+                                     (200, 1, 1, 1 << 20), (170, 7, 4, 1 << 19), (40, 200, 1, 1 << 20),
+                                     (1, 9728, 4, 40960), (1, 9728, 4, 71680), (300, 1, 1, 66560), (200, 7, 4, 133120)])
 def test_paged_attn_sums_do_not_shrink_with_the_context(cas, B, T, G, n):
     """Units of up to 32768 key tiles, one page throughout: the tensor cores' sums
     must not lose what grows with the number of tiles.
@@ -463,6 +464,21 @@ def test_paged_attn_sums_do_not_shrink_with_the_context(cas, B, T, G, n):
     print("mean", (err.sum() / mass.sum()).item())
     assert (err.abs() <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -12) * mass + 2.0 ** -8 * ref.abs()).all()
     assert err.sum().abs() <= (2.0 ** -11 + 2.0 ** -13) * mass.sum()
+
+
+@pytest.mark.parametrize("B,T,G", [(1, 9728, 4), (200, 7, 4)])
+def test_paged_attn_long_units_and_values_that_a_row_does_not_see(cas, B, T, G):
+    """Units of 560 tiles whose last token's value is not finite."""
+    page, n = 1024, 71680
+    k, v = pools(2, page, 1, "tokens", seed=5)
+    q = torch.randn(B * T, G, D, device="cuda").to(BF)
+    args = dev32([T * b for b in range(B + 1)], [n] * B, [[0] * (n // page - 1) + [1]] * B)
+    clean = cas.paged_attn(q, k, v, *args).view(BF)
+    v[1, page - 1, 0, 77] = float("nan")
+    got = cas.paged_attn(q, k, v, *args).view(BF)
+    hit = torch.zeros_like(got, dtype=torch.bool)
+    hit[T - 1::T, :, 77] = True
+    assert got[hit].isnan().all() and torch.equal(got[~hit], clean[~hit])
 
 
 def test_paged_attn_offsets_beyond_32_bits(cas):
