@@ -717,9 +717,16 @@ def _call(fn, what: str, index: int, *args):
 def _with_stream(stream, t: torch.Tensor, fn, *args):
     """fn(*args) with `stream` current: buffers that it makes, results among
     them, come from that stream's memory, so that no other stream reuses them
-    under a kernel, and copies that it makes are ordered with the kernel."""
+    under a kernel, and copies that it makes are ordered with the kernel. The
+    tensors that it is given are recorded on the stream: a caller may drop them
+    when the call returns. (Their memory, reused by their own stream under a
+    kernel that reads lengths or page tables from it, would let its warps see
+    different ones.)"""
     if not t.is_cuda or stream.device != t.device:
         raise ValueError(f"libcas takes device tensors of the stream's device: got {t.device}")
+    for a in args:
+        if isinstance(a, torch.Tensor) and a.is_cuda:
+            a.record_stream(stream)
     with torch.cuda.stream(stream):
         return fn(*args)
 
