@@ -146,7 +146,7 @@ struct Shape {
     float m[kWarps][kUnit], l[kWarps][kUnit];
     uint64_t full[kStages], empty[kStages];
     uint32_t done[kStages], loads[kStages];  // warps through with a stage's tiles, tiles loaded
-    uint64_t walk[12];
+    uint64_t walk[12], next[4];
     int abort;
   };
   static_assert(kCtas * (sizeof(Smem) + 1024) <= 233472, "shared memory of an SM");
@@ -175,12 +175,20 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t phase, int* abort) 
 }
 
 // The units of a CTA, or its parts of them. One warp finds the first; then every warp
-// walks them by itself. N: what counts cells.
+// walks them by itself, but one thread looks at the lengths of the sequences that follow
+// for all computing warps: these meet at barriers whose number hangs on the units, so every
+// one of them has to see the same lengths, also where a caller changes them under the
+// kernel (the output then means nothing). N: what counts cells.
 struct Unit {
   int b, start, hk, f0, rows;  // sequence and its first row, kv head, flat rows
   int pos0, kv_end;            // position of the sequence's first row, end of what it holds
   int t0, n, all;              // key tiles of this CTA, of the unit
   bool first, last;            // of this CTA's
+};
+// A sequence that has rows; b = batch: there is none.
+struct NextSeq {
+  int b;
+  Seq s;
 };
 template <int NT, class N>
 struct Walk {
@@ -215,13 +223,23 @@ struct Walk {
     cell = 0;
     return w;
   }
-  __device__ __forceinline__ void next(const LineArgs& a) {
+  // Whether the next unit lies in another sequence, and that sequence.
+  __device__ __forceinline__ bool leaves(const LineArgs& a) const {
+    return p.qt + 1 >= L::unit_count(s) && p.hk + 1 >= a.d.H;
+  }
+  __device__ __forceinline__ NextSeq look(const LineArgs& a) const {
+    NextSeq n{p.b, Seq{}};
+    do n.s = ++n.b < a.d.batch ? seq_of(a, n.b) : Seq{};
+    while (n.s.R == 0 && n.b < a.d.batch);
+    return n;
+  }
+  __device__ __forceinline__ void next(const LineArgs& a, const NextSeq& n) {
     if (++p.qt < L::unit_count(s)) return;
     p.qt = 0;
     if (++p.hk < a.d.H) return;
     p.hk = 0;
-    do s = ++p.b < a.d.batch ? seq_of(a, p.b) : Seq{};
-    while (s.R == 0 && p.b < a.d.batch);
+    p.b = n.b, s = n.s;
+    any = p.b < a.d.batch;
   }
 };
 
@@ -630,9 +648,13 @@ __device__ void compute(const P4Args& a, const CUtensorMap* map, typename Shape<
         }
       }
     }
+    // (read behind this meeting, written behind the one of the unit's first rows)
+    NextSeq& following = *reinterpret_cast<NextSeq*>(x->next);
+    if (threadIdx.x == 0 && !w.last && walk.leaves(a)) following = walk.look(a);
+    __syncwarp();
     meet();  // what is shared is read before the next unit's is written
     if (w.last) break;
-    walk.next(a);
+    walk.next(a, following);
   }
   if (threadIdx.x == 0) {
     cut.ok = 1;  // (taken back where a wait gave up)
@@ -656,7 +678,7 @@ __device__ void produce(const P4Args& a, const CUtensorMap* map, typename Shape<
       if (++slot == kStages) slot = 0, phase ^= 1;
     }
     if (w.last) return;
-    walk.next(a);
+    walk.next(a, walk.leaves(a) ? walk.look(a) : NextSeq{});
   }
 }
 
@@ -667,7 +689,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, Shape<NT>::kCtas)
   extern __shared__ __align__(1024) uint8_t smem[];
   auto* x = reinterpret_cast<typename Sh::Smem*>(smem);
   Walk<NT, N>& walk = *reinterpret_cast<Walk<NT, N>*>(x->walk);
-  static_assert(sizeof(walk) <= sizeof(x->walk), "room for the walk");
+  static_assert(sizeof(walk) <= sizeof(x->walk) && sizeof(NextSeq) <= sizeof(x->next), "room for the walk");
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::kStages; ++i) {

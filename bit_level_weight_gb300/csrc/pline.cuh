@@ -204,8 +204,9 @@ __global__ void __launch_bounds__(kJoinThreads, CTAS) attn_join_kernel(const __g
   pdl_wait();
   pdl_trigger();
   const int at = blockIdx.x;
-  const Cut cut = a.cuts[at];
+  Cut cut = a.cuts[at];
   const int ctas = a.ctas - at;  // from the cut's on
+  cut.pieces = min(cut.pieces, ctas);  // (more only where lengths changed while the pieces were made)
   bool ok = threadIdx.x >= ctas || a.cuts[at + threadIdx.x].ok || threadIdx.x >= cut.pieces;
   if (cut.pieces < 2) return;
   for (int k = threadIdx.x + kJoinThreads; k < cut.pieces; k += kJoinThreads) ok = ok && a.cuts[at + k].ok;
