@@ -99,7 +99,8 @@ __device__ void plan_rows(const PlanArgs& a, int64_t i0, int64_t n, int used, in
     const int64_t at = height - 1 - k;
     return at >= 0 ? a.free_pages[at] : 0;  // (the sums keep k below the height)
   };
-  for (int64_t r = i0; r < a.rows; r += n) {
+  const int rows = a.pos || a.slot ? a.rows : used;  // (else those behind them are nowhere written)
+  for (int64_t r = i0; r < rows; r += n) {
     int pos = -1;
     int64_t slot = -1;
     if (r < used) {
@@ -223,7 +224,7 @@ extern "C" int cas_paged_plan(const cas_page_pool* pool, const int32_t* keep, co
   const bool one = rows <= kRowsOfOneCta;
   if (const int e = launch_k(plan_seq_kernel, 1, kThreads, 0, st, a, one)) return e;
   if (one) return CAS_OK;
-  const int blocks = std::min((rows + kRowThreads - 1) / kRowThreads, sm_count() * 8);
+  const int blocks = (int)std::min<int64_t>(((int64_t)rows + kRowThreads - 1) / kRowThreads, sm_count() * 8);
   // directly behind our own kernel: its launch may overlap that kernel's tail
   return launch_with(true, plan_rows_kernel, dim3(blocks), kRowThreads, 0, st, a);
 }
