@@ -16,6 +16,8 @@
 #define CAS_FULL 0xFFFFFFFFu
 #define CAS_BLK 128
 #define CAS_SB 8
+// Sequences of a ragged batch: kernels go over them in rounds of up to 1024, in 32 bits.
+#define CAS_MAX_BATCH (0x7FFFFFFF - 1024)
 
 namespace cas {
 

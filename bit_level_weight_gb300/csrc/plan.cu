@@ -206,7 +206,7 @@ extern "C" uint64_t cas_paged_plan_workspace_bytes(int batch) {
 extern "C" int cas_paged_plan(const cas_page_pool* pool, const int32_t* keep, const int32_t* add, int rows,
                               int32_t* row_start, int32_t* granted, int32_t* pos, int64_t* slot, void* workspace,
                               uint64_t workspace_bytes, void* stream) {
-  if (!pool || rows < 0 || pool->batch < 0 || pool->max_pages < 1 || pool->n_pages < 1) return CAS_ERR_INVALID;
+  if (!pool || rows < 0 || pool->batch < 0 || pool->batch > CAS_MAX_BATCH || pool->max_pages < 1 || pool->n_pages < 1) return CAS_ERR_INVALID;
   const int S = pool->page_size;
   if (S < 8 || S > 1024 || (S & (S - 1)) || (int64_t)pool->max_pages * S > 0x7FFFFFFF) return CAS_ERR_INVALID;
   if (!row_start || !pool->n_free || !pool->free_pages || (pool->batch > 0 && (!pool->pages || !pool->kv_len || !add)))

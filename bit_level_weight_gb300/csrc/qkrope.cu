@@ -54,7 +54,7 @@ PagedDev paged_dev(const KV* kv, const cas_paged_batch* b) {
 }
 template <class KV>
 bool good_paged(const KV* kv, const cas_paged_batch* b, int64_t least_stride, int64_t stride_unit) {
-  if (!kv || !b || b->batch < 0 || b->rows < 0 || b->max_pages < 1) return false;
+  if (!kv || !b || b->batch < 0 || b->batch > CAS_MAX_BATCH || b->rows < 0 || b->max_pages < 1) return false;
   const int S = kv->page_size;
   if (kv->n_kv_heads < 1 || kv->n_kv_heads > 4096 || S < 8 || S > 1024 || (S & (S - 1)) || kv->n_pages < 1 ||
       kv->n_pages > 0x7FFFFFFF)

@@ -561,8 +561,8 @@ typedef struct cas_paged_batch {
  * token's slots, q to [rows][n_q_heads][128]. Two rows must not share a slot,
  * and nothing written may overlap an input.
  * Errors: those of cas_qk_norm_rope; CAS_ERR_INVALID for a null descriptor
- * or pointer, a page size, stride or alignment out of range, batch < 0 or
- * max_pages < 1. rows = 0 or batch = 0 does nothing. */
+ * or pointer, a page size, stride or alignment out of range, batch < 0 or above
+ * 2^31 - 1025, or max_pages < 1. rows = 0 or batch = 0 does nothing. */
 int cas_paged_append(const cas_paged_kv* kv, const cas_paged_batch* b, const void* qkv, int qkv_type, int n_q_heads,
                      const uint16_t* gamma_q, const uint16_t* gamma_k, float eps, double theta, uint16_t* q,
                      void* stream);
@@ -689,8 +689,8 @@ typedef struct cas_page_pool {
  * hold is lost; page ids are not looked at, so a place's slot is as wide as its
  * id. pages, kv_len, free_pages, n_free, inputs and outputs must not overlap.
  * Calls that may overlap on the GPU need a workspace each (and a pool).
- * Errors: CAS_ERR_INVALID for a null descriptor, batch or rows < 0, max_pages < 1
- * or max_pages * page_size above 2^31 - 1, a page size as in cas_paged_kv,
+ * Errors: CAS_ERR_INVALID for a null descriptor, batch or rows < 0, batch above
+ * 2^31 - 1025, max_pages < 1 or max_pages * page_size above 2^31 - 1, a page size as in cas_paged_kv,
  * n_pages < 1, or a null pointer; CAS_ERR_BUFFER if the workspace is null, not
  * 16-byte aligned or smaller than cas_paged_plan_workspace_bytes; CAS_ERR_CUDA.
  * batch = 0 writes row_start[0] and marks all rows as unused. */

@@ -6,6 +6,7 @@ import torch
 
 import bit_level_weight_gb300 as cas
 
+GOOD = 0x10000  # a 16-byte aligned address that no refused call touches
 MOST = 2 ** 31 - 1
 
 
@@ -13,6 +14,22 @@ def built():
     from bit_level_weight_gb300 import build
     build.build()
     return cas.lib()
+
+
+@pytest.mark.parametrize("batch", [MOST, MOST - 1023])
+def test_batches_whose_rounds_pass_32_bits_are_refused(batch):
+    """Kernels go over the sequences in rounds of up to 1024, counted in 32 bits."""
+    L = built()
+    pool = cas.cas_page_pool(batch, 3, 16, 8, GOOD, GOOD, GOOD, GOOD)
+    assert L.cas_paged_plan(ctypes.byref(pool), None, GOOD, 4, GOOD, None, None, None, GOOD, 1 << 62, None) == -1
+    b = ctypes.byref(cas.cas_paged_batch(batch, 2, 3, 0, GOOD, GOOD, GOOD))
+    kv = ctypes.byref(cas.cas_paged4_kv(2, 16, 8, GOOD, 16 * 288, 288, 144))
+    assert L.cas_paged4_append(kv, b, GOOD, 0, 4, None, None, 1e-6, 1e4, GOOD, None) == -1
+    assert L.cas_paged4_read(kv, b, GOOD, GOOD, None) == -1
+    assert L.cas_paged4_attn(kv, b, GOOD, 4, GOOD, GOOD, 1 << 62, None) == -1
+    kv = ctypes.byref(cas.cas_paged_kv(2, 16, 8, GOOD, GOOD, 16 * 256, 256, 128))
+    assert L.cas_paged_append(kv, b, GOOD, 0, 4, None, None, 1e-6, 1e4, GOOD, None) == -1
+    assert L.cas_paged_attn(kv, b, GOOD, 4, GOOD, GOOD, 1 << 62, None) == -1
 
 
 def pool_on_gpu():
