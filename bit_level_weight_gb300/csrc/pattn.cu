@@ -617,9 +617,14 @@ __device__ bool guard_values(const Unit& w, uint32_t u, int slot, int key0, uint
   return true;
 }
 
+// A maximum is rounded once, by up to 2^-24 of itself, and the scores that it is taken from are not: up to
+// here that makes all of a row's P alike wrong by 2^(2^-4), beyond it too large or zero.
+constexpr float kFar = 0x1p20f;
+
 // P = 2^(s kScaleLog2 - ref) of a row's 128 scores as bf16 into its columns at
-// tm_s, with LOW what the rounding left of it behind; returns the sum of P.
-template <bool LOW>
+// tm_s, with LOW what the rounding left of it behind; returns the sum of P. FAR: a
+// ref beyond kFar is taken from scores that are rounded as it was.
+template <bool LOW, bool FAR = false>
 __device__ __forceinline__ float weigh_keys(const uint32_t s[kTile], float ref, uint32_t tm_s) {
   const uint64_t sc2 = pack2(kScaleLog2, kScaleLog2), ref2 = pack2(-ref, -ref);
   uint64_t ls[2] = {0, 0};
@@ -630,6 +635,10 @@ __device__ __forceinline__ float weigh_keys(const uint32_t s[kTile], float ref, 
     for (int k = 0; k < 32; ++k) {
       float e0, e1;
       unpack2(fma2(pack2(__uint_as_float(s[64 * c + 2 * k]), __uint_as_float(s[64 * c + 2 * k + 1])), sc2, ref2), e0, e1);
+      if (FAR && fabsf(ref) > kFar) {
+        e0 = __fadd_rn(__fmul_rn(__uint_as_float(s[64 * c + 2 * k]), kScaleLog2), -ref);
+        e1 = __fadd_rn(__fmul_rn(__uint_as_float(s[64 * c + 2 * k + 1]), kScaleLog2), -ref);
+      }
       e0 = ex2(e0);
       e1 = ex2(e1);
       ls[k & 1] = add2(ls[k & 1], pack2(e0, e1));
@@ -642,6 +651,22 @@ __device__ __forceinline__ float weigh_keys(const uint32_t s[kTile], float ref, 
   float l0, l1;
   unpack2(add2(ls[0], ls[1]), l0, l1);
   return l0 + l1;
+}
+
+// The same of a warp that has a row with its maximum beyond kFar: rare, and apart, as the loop over the tiles has
+// no registers left. The scores are read again; the last that the row sees is number `last`. (The look for such
+// rows takes 2048 rows over 32K of the 4-bit cache from 746 to 759 us, of the bf16 cache nothing.)
+template <bool LOW>
+__device__ __noinline__ float weigh_far_keys(float ref, uint32_t tm_s, int last) {
+  uint32_t s[kTile];
+#pragma unroll
+  for (int c = 0; c < kTile; c += 32) tm_ld32(s + c, tm_s + c);
+#pragma unroll
+  for (int c = 0; c < kTile; c += 32) tm_wait_ld(s + c);
+#pragma unroll
+  for (int c = 0; c < kTile; ++c)
+    if (c > last) s[c] = 0xFF800000u;
+  return weigh_keys<LOW, true>(s, ref, tm_s);
 }
 
 // The tensor cores cut their sums, so a slot's O takes kFold tiles at most: then
@@ -778,7 +803,9 @@ __device__ void softmax(const AttnArgs& a, uint8_t* ring, Aux* x) {
           }
           const float ref = m == -INFINITY ? 0.f : m;
           // (what is expected lies in the loop: one token over 32K 40.8 us, 41.8 the other way round)
-          if (LOW && __builtin_expect(!two, 1))
+          if (__builtin_expect(__any_sync(CAS_FULL, fabsf(ref) > kFar), 0))
+            l += LOW && !two ? weigh_far_keys<LOW>(ref, tm_s, last) : weigh_far_keys<false>(ref, tm_s, last);
+          else if (LOW && __builtin_expect(!two, 1))
             l += weigh_keys<true>(s, ref, tm_s);
           else
             l += weigh_keys<false>(s, ref, tm_s);
