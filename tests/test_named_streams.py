@@ -69,3 +69,24 @@ def test_memory_of_dropped_arguments_is_not_reused_under_a_call(which):
     del out
     again = [make() for _ in range(4)]  # behind the call the memory is free again
     assert at in [x.data_ptr() for x in again]
+
+
+@pytest.mark.gpu
+def test_a_call_on_a_named_stream_is_captured():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from bit_level_weight_gb300 import build
+    build.build()
+    x = torch.randn(3, 1, 5000, device="cuda")
+    bias = (torch.tensor([0, 1, 1, 2], dtype=torch.int32, device="cuda"), torch.tensor([7, 4000], dtype=torch.int32, device="cuda"),
+            torch.tensor([2.0, float("-inf")], device="cuda"))
+    want = cas.adjust_logits(x, bias_start=bias[0], bias_token=bias[1], bias_value=bias[2])
+    out, st, graph = torch.zeros_like(x), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=st):
+        cas.adjust_logits(x, bias_start=bias[0], bias_token=bias[1], bias_value=bias[2], out=out, stream=st)
+    assert not out.any()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.isneginf(out[2, 0, 4000]) and out[0, 0, 7] == x[0, 0, 7] + 2
