@@ -32,8 +32,6 @@ constexpr uint32_t kScaleBias = 0x35803580u;  // 2^-20 in both halves
 
 // Twice the scale byte `b` (0..255) as bf16.
 __device__ __forceinline__ uint32_t q4_scale2(uint32_t b) { return b * 0x00100010u + kScaleBias; }
-// The scale bytes a (lower half) and b.
-__device__ __forceinline__ uint32_t q4_scale_pair(uint32_t a, uint32_t b) { return (a << 4) + (b << 20) + kScaleBias; }
 __device__ __forceinline__ uint32_t q4_fma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
