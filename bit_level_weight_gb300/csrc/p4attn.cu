@@ -7,10 +7,12 @@
 //
 // The products are transposed, so that keys are the long side of a tensor core
 // product and few rows its short one: S^T = K Q^T and O^T = V^T P^T with
-// mma.m16n8k16, 8 rows a product. tcgen05 would take 128 rows for 4: 512 clocks a
-// product and 1024 a tile, where a tile's 18 KB take 800 of the memory. Here the codes
-// become fp16 in the registers that the product reads, and pass through shared
-// memory once, as codes.
+// mma.m16n8k16, 8 rows a product. The codes become fp16 in the registers that the
+// product reads, and pass through shared memory once, as codes. That pipe makes 1024
+// multiply-adds a clock and SM: a tile of 128 keys takes 256 of its clocks for 8 rows,
+// 512 for 16 and 1024 for 32, where the tile's 18 KB take 865 of the memory. So up to 16
+// rows the memory may bound it; 32 rows would have to go through tcgen05, with the keys
+// on its side of 128, and through a copy of K and V as 16-bit values. That is not done.
 //
 // A warp takes 32 keys of a tile. In a product's A operand lane (g, t) holds rows
 // g and g + 8 and the columns 2t, 2t + 1, 2t + 8, 2t + 9; which keys and dimensions
@@ -33,16 +35,19 @@
 // by tiled TMA, which takes rows of 144 bytes one by one.
 //
 // What bounds it (measured on GB300, 8 kv heads, 32 query heads):
-//   one token a sequence: 61 ragged sequences of up to 8K in 66 us for 282 MB, of which 12
-//     are the start, the ends of units and the join; in between 5.7 TB/s, 86 % of the
-//     measured copy rate, at 56 % of the issue slots (310 instructions of a warp for 16
-//     keys). With tiled TMA 86 us, without the loading warp (and a CTA more an SM) 88, with
-//     bf16 operands and P in two terms 86, with one CTA of 16 warps an SM 139.
+//   one token a sequence: 61 ragged sequences of up to 8K in 66 us for 282 MB, 4.3 TB/s. Twice
+//     the lengths take 114 us and four times 212: what comes on top runs at 5.7-5.9 TB/s,
+//     86-88 % of the measured copy rate, at 57 % of the issue slots (310 instructions of a warp
+//     for 16 keys), and 17 us are the start, the ends of units and the join. With tiled TMA 86
+//     us, without the loading warp (and a CTA more an SM) 88, with bf16 operands and P in two
+//     terms 86, with one CTA of 16 warps an SM 139.
 //   one token over 32K: 20 us for 38 MB, 10 to the first tile and 5 for the join.
-//   7 rows of 4 heads: units of 32 rows hold 240 registers a thread, so that two warps a
-//     scheduler have to hide their products' and logic's latencies: 2.2 TB/s, the products'
-//     pipe 42 % busy (2 x 7 rows over 16K: 33 us). The kernel of long chunks takes 10 % more
-//     for 32 x 7 rows over 16K.
+//   4 rows of 4 heads (units of 16): 32 sequences of 8K in 102 us for 302 MB, 3.0 TB/s; of 16K
+//     in 179. The products' pipe is 32 % busy, the issue slots 47 %.
+//   7 rows of 4 heads: units of 32 rows hold 242 registers a thread, so that two warps a
+//     scheduler have to hide their products' and logic's latencies: 32 sequences of 8K in 150
+//     us, 2.0 TB/s, the products' pipe 42 % busy (2 x 7 rows over 16K: 33 us). The kernel of long
+//     chunks takes 10 % more for 32 x 7 rows over 16K.
 //
 // Every wait is bounded as in pattn.cu; a CTA whose wait gave up writes no output
 // and its units' pieces are not joined.
@@ -75,7 +80,8 @@ struct ReadArgs {
   PagedDev d;
   uint16_t *k, *v;
 };
-// A warp takes four heads of a row, eight lanes a head, 16 dimensions of K and V a lane.
+// A warp takes four heads of a row, eight lanes a head, 16 dimensions of K and V a lane. Bound by
+// the chain row bounds -> page -> record (2048 rows of 8 heads 4.9 us for 10.7 MB, 14 rows 2.8).
 constexpr int kReadThreads = 128;
 __device__ __forceinline__ void put16(uint16_t* to, uint2 codes, uint32_t scale) {
   const Q4Bf16 q4;
@@ -133,7 +139,10 @@ struct Shape {
   static constexpr int kUnit = 8 * NT;
   static constexpr bool kLoads = NT == 1;            // a warp that loads
   static constexpr int kThreads = 32 * kWarps + (kLoads ? 32 : 0);
-  static constexpr int kCtas = NT == 4 ? 2 : 3;      // an SM, of 128, 168, 255 registers a thread
+  // CTAs an SM, of 128, 168, 255 registers a thread. Units of 8 rows spill 48 bytes a thread, of 16 rows 40: a
+  // variant with 0 and 20 took 64.4 instead of 65.3 us (61 ragged tokens) and 97.6 instead of 101.8 (32 x 4 rows
+  // over 8K), but units of 32 rows, which spill nothing either way, 153 instead of 150 (32 x 7 rows).
+  static constexpr int kCtas = NT == 4 ? 2 : 3;
   static constexpr int kStages = NT == 4 ? 4 : 3;
   static constexpr int kHalves = NT <= 2 ? 2 : 1;    // of 16 keys that a warp takes in a step
   static constexpr bool kQShared = NT > 2;           // Q's operands in shared memory instead of registers
@@ -733,7 +742,14 @@ bool make_map(CUtensorMap* m, const cas_paged4_kv* kv) {
 }
 
 // Units of 8, 16 or 32 rows: the least that hold a sequence's flat rows on average; 0:
-// more than 32, for pattn.cu's units of 256.
+// more than 32, for pattn.cu's units of 256. The host knows no more than rows and
+// sequences. (At the border, of 4 heads over 8K: 32 x 8 rows take 151 us here, 32 x 9 in
+// units of 256 179.) What the average hides costs time, not results: a sequence far above it
+// has its keys read again by every small unit, and sequences without rows lower it. 2048 rows
+// over 32K take 760 us alone or beside 63 empty sequences, 3900 us beside 255 and 6300
+// beside 1023; 63 single tokens over 8K with a chunk of 448 rows over 32K 1170 us, with one of 451
+// (the long chunks' kernel for all) 600. A caller whose table has many empty places had better pass
+// the sequences that have rows.
 int units_of(int64_t flat, int64_t batch) {
   return flat <= 8 * batch ? 1 : flat <= 16 * batch ? 2 : flat <= 32 * batch ? 4 : 0;
 }

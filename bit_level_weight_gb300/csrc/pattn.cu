@@ -50,7 +50,8 @@
 //
 // The 4-bit cache (cas_paged4_attn, more than 32 rows of a kv head a sequence): the same
 // with a fourth warpgroup that writes the tiles which TMA writes here: 2048 rows over 32K
-// in 740 us = 1.44 PFLOP/s. (By the two loading warps: 2711 us.)
+// in 759 us = 1.40 PFLOP/s. (By the two loading warps: 2711 us.) Its softmax spills 76 bytes
+// a thread.
 //
 // Every wait is bounded: one that gives up marks the CTA, whose warps then
 // leave their loops, and sets a status that cas_device_status reads. Units that
@@ -96,7 +97,7 @@ constexpr int kLowPart = kTile / 2;        // columns of S behind P
 constexpr int kThreads = 384;               // three warpgroups of 168 registers a thread at launch
 constexpr int kThreads4 = 512;              // four of 128
 // Registers of the softmax, which keeps a row of S, and of the others: 2 * 216 + 72 = 3 * 168. With the
-// 4-bit cache's decoders, a fourth warpgroup: 2 * 184 + 72 + 72 = 4 * 128 (with 2 * 176 + 88 the softmax spills: 836 instead of 740 us).
+// 4-bit cache's decoders, a fourth warpgroup: 2 * 184 + 72 + 72 = 4 * 128 (with 2 * 176 + 88 the softmax spills more: 836 instead of 740 us).
 template <bool Q4>
 struct Regs {
   static constexpr int kSoftmax = Q4 ? 184 : 216, kOther = 72, kDecode = 72;

@@ -11,8 +11,10 @@
 // What bounds it: many rows, the traffic (fp32 rows of 13 ragged sequences into
 // pages: 35 us for 204 MB = 5.8 TB/s, 86 % of the measured copy rate; 4096 bf16
 // rows: 22.6 us for 101 MB = 4.5 TB/s, where half of the issue slots are taken);
-// a few rows, the launch (5-6 us). Into records, issue: a true division a value and the
-// packing of codes (2048 bf16 rows 18 us for 32 MB, 2224 fp32 rows 20 us for 80 MB).
+// a few rows, the launch (5-6 us). Into records, neither: a true division a value and the
+// packing of codes by 20 to 24 warps an SM (96 and 80 registers a thread), whose latencies
+// they do not hide: 2048 bf16 rows 21 us for 44 MB (2.1 TB/s, 53 % of the issue slots), 2224
+// fp32 rows 21 us for 75 MB (3.6 TB/s, 39 %).
 //
 // Angle: theta^(-i/64) / 2 pi is a fraction of a turn per position, held as a
 // 64-bit fixed-point number f_i in units of 2^-64 turns, the product of two

@@ -120,9 +120,9 @@ int cas_device_status(void* stream);
  * cas_device_status), wait once more with the normal limit so the copy lands
  * before the block exits, and write no output. This sets the limit of that
  * first wait for later launches: 0 makes it give up at once, 0xFFFFFFFF
- * restores the normal limit. With 0, cas_paged_attn's warps also wait for work
- * that is never handed out, give up, record CAS_ERR_TIMEOUT and write no
- * output; with 1, those of every second CTA do, and rows that need such a CTA's
+ * restores the normal limit. With 0, cas_paged_attn's and cas_paged4_attn's
+ * warps also wait for what never comes, give up, record CAS_ERR_TIMEOUT and write
+ * no output; with 1, those of every second CTA do, and rows that need such a CTA's
  * part stay as they were. Synchronises the device; returns CAS_OK or
  * CAS_ERR_CUDA. */
 int cas_test_first_wait_spins(uint32_t spins);
@@ -638,7 +638,10 @@ int cas_paged4_read(const cas_paged4_kv* kv, const cas_paged_batch* b, uint16_t*
  * positions up to and including the row's own, K and V the values that the
  * records stand for. q, o, GQA, ragged batches, rows that see no key and what
  * lies at positions that a row does not see: as there, but nothing in the cache
- * can be infinite. A row has an output that means nothing where its q is not
+ * can be infinite. The three arrays of the batch may change between calls (and
+ * between replays of a graph), not under one. The kernel is chosen by the average of
+ * rows * n_q_heads / n_kv_heads over `batch` sequences: many sequences without rows
+ * beside a long chunk, or one far above the average, cost time. A row has an output that means nothing where its q is not
  * finite or where it sees a record whose scale bytes the append does not write
  * (cas_paged4_read takes those too); other rows are not touched by it. fp32
  * scores, statistics and sums; probabilities in fp16 where rows * n_q_heads /
@@ -687,7 +690,9 @@ typedef struct cas_page_pool {
  * n_free keep what they hold. kv_len outside 0..max_pages * page_size and n_free
  * outside 0..n_pages count as the nearest value inside, and what the stack cannot
  * hold is lost; page ids are not looked at, so a place's slot is as wide as its
- * id. pages, kv_len, free_pages, n_free, inputs and outputs must not overlap.
+ * id, and a page that two sequences hold (a shared prefix) or that is on the stack
+ * too comes back, and is given out, once for each: a caller who shares pages keeps
+ * them out of what is dropped. pages, kv_len, free_pages, n_free, inputs and outputs must not overlap.
  * Calls that may overlap on the GPU need a workspace each (and a pool).
  * Errors: CAS_ERR_INVALID for a null descriptor, batch or rows < 0, batch above
  * 2^31 - 1025, max_pages < 1 or max_pages * page_size above 2^31 - 1, a page size as in cas_paged_kv,
