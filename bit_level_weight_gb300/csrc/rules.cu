@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(kRuleThreads, 1024 / kRuleThreads) rules_kerne
   };
   if (penal) take(t, (int)(max(a.r.max_history - to16, (int64_t)0) / 4));
   const int drafts = drafts_of(a, b);
-  if (t <= drafts) masks[t] = mask_of(a, (int64_t)b * a.rows + t);
+  // (of all rows: a thread that saw another n_draft, changed under the kernel, finds a mask or none)
+  if (t < a.rows) masks[t] = mask_of(a, (int64_t)b * a.rows + t);
   // (token ids outside the vocabulary are none of the slice's n, negative ones neither)
   auto place = [&](int32_t token) { return (uint32_t)token - (uint32_t)w0; };
   if (t < drafts) xs[t] = penal && a.x ? place(a.x[(int64_t)b * a.x_stride + t]) : 0xFFFFFFFFu;
